@@ -449,6 +449,109 @@ int32_t trellis_encode(int32_t n_tiles, int32_t k_bits, int32_t code_id, float s
 /* Workspace bytes for trellis_encode (0 if the arguments are invalid). */
 size_t tg_encode_workspace_size(int32_t n_tiles, int32_t k_bits, int32_t code_id);
 
+/* Element types of the routing and 8-bit entry points. */
+#define TG_F32 0
+#define TG_F16 1
+#define TG_BF16 2
+
+/* moe_route flags. */
+#define TG_ROUTE_SIGMOID 1  /* scores 1 / (1 + exp(-l)) instead of a softmax over the experts */
+#define TG_ROUTE_RENORM 2   /* the selected scores are divided by their sum */
+
+/*
+ * Routing of tokens to experts (Deep Dive, Section 4: the expert models that trellis_moe_block and
+ * trellis_gemv_grouped serve take their ids and weights from it):
+ *     s = softmax(l) or sigmoid(l) over the token's logits l,
+ *     r = s + bias (bias for balance: it takes part in the selection and never in the weights),
+ *     ids = the top_k experts by r -- by l itself where there is no bias, which is the same order --
+ *           in falling order, equal ones by their index,
+ *     w   = scale * s[ids], with TG_ROUTE_RENORM scale * s[ids] / sum(s[ids]).
+ * With n_group > 1 the experts form n_group equal neighbouring groups; a group's value is the largest
+ * r in it (group_top 1) or the sum of its two largest (group_top 2), and only experts of the topk_group
+ * groups of largest value are selected (equal ones by their index). Scores, values and comparisons are
+ * formed in binary64; a weight is rounded to binary32 once.
+ * An expert whose logit or bias is -infinity is not available: it is never selected, and a group value
+ * sums over the available ones (a group without any is not selected). Slots left over when fewer than
+ * top_k experts are available get id -1 and weight 0, which trellis_moe_block, trellis_gemv_grouped and
+ * moe_group take as "no expert". A token with a NaN logit, with a logit of +infinity under softmax, or
+ * with a bias that is NaN or +infinity gets the ids 0 .. top_k-1 and NaN weights.
+ *   tokens  : 1 .. 2^24; experts : 1 .. 1024; top_k : 1 .. min(64, experts).
+ *   logits  : device, tokens rows of experts values of type dtype (TG_F32, TG_F16, TG_BF16), row stride
+ *             ld >= experts elements.
+ *   bias    : device, experts fp32, or NULL.
+ *   n_group : divides experts, at most 64; topk_group : 1 .. n_group; group_top : 1 or 2.
+ *             topk_group * (experts / n_group) >= top_k.
+ *   scale   : finite.
+ *   sel     : device, tokens * top_k int32 out; weights : device, tokens * top_k fp32 out.
+ */
+int32_t moe_route(int32_t tokens, int32_t experts, int32_t top_k, const void *logits, int32_t dtype, int64_t ld,
+                  const float *bias, int32_t n_group, int32_t topk_group, int32_t group_top, int32_t flags,
+                  float scale, int32_t *sel, float *weights, void *stream);
+
+/*
+ * The routed pairs in expert order, which int8_gemm_grouped reads: pair p = token * top_k + slot with
+ * expert sel[p]; order lists the pairs by expert, each expert's in rising p, and behind them the pairs
+ * whose id lies outside [0, experts); expert e's are order[offsets[e] .. offsets[e + 1] - 1].
+ *   pairs   : 1 .. 2^24; experts : 1 .. 1024.
+ *   sel     : device, pairs int32.
+ *   offsets : device, experts + 1 int32 out; order : device, pairs int32 out.
+ */
+int32_t moe_group(int32_t pairs, int32_t experts, const int32_t *sel, int32_t *offsets, int32_t *order, void *stream);
+
+/*
+ * 8-bit rows with a scale for each row: amax = max_i |x_i|, scale = amax / 127, q_i = the whole number
+ * nearest to 127 x_i / amax (an exact half to the even one), so x_i is about q_i * scale and
+ * |q_i| <= 127. The quotient's rounding is decided exactly; scale is rounded once. A row of zeros gets
+ * scale 0 and zeros; a row with a NaN or an infinity gets scale NaN and zeros, so its products are NaN.
+ * Rows of a weight matrix give an 8-bit layer with a scale for each output channel.
+ *   rows : 1 .. 2^24; n : 1 .. 2^22.
+ *   x    : device, rows of n values of type dtype, row stride ldx >= n elements.
+ *   q    : device, rows of n int8 out, row stride ldq >= n bytes (what lies between rows is left as it was).
+ *   scales : device, rows fp32 out.
+ */
+int32_t int8_quantize(int32_t rows, int32_t n, const void *x, int32_t dtype, int64_t ldx, int8_t *q, int64_t ldq,
+                      float *scales, void *stream);
+
+/*
+ * Matrix product in 8-bit integers with a scale for each activation row and output channel, on the matrix
+ * cores (for layers kept at 8 bits beside the trellis-coded ones; lecture, Part eleven on int8 activations):
+ *     Y[r, o] = (sum_i xq[r, i] * wq[o, i]) * xs[r] * ws[o].
+ * The sums are exact (int32); an output is rounded in binary32 as it is written here, and once more to a
+ * 16-bit out_dtype.
+ *   M  : 1 .. 2^20 rows; m : 1 .. 2^22 outputs; n : a multiple of 16 up to 131056 (so that no sum leaves
+ *        int32, 128 * 128 * n < 2^31).
+ *   xq : device, M rows of n int8, 16-byte aligned, row stride ldx >= n bytes, a multiple of 16.
+ *   xs : device, M fp32. wq : device, m rows of n int8, aligned as xq. wscales : device, m fp32.
+ *   Y  : device, M rows of m values of type out_dtype, row stride ldy >= m elements.
+ *   ws : device workspace, ws_bytes >= tg_int8_workspace_size(M, m, n), 256-byte aligned, zero-filled
+ *        before its first use; every call leaves its counters at zero, so one buffer, as large as each
+ *        product needs, serves any sequence of products on one stream.
+ */
+int32_t int8_gemm(int32_t M, int32_t m, int32_t n, const int8_t *xq, int64_t ldx, const float *xs,
+                  const int8_t *wq, int64_t ldw, const float *wscales, void *Y, int32_t out_dtype, int64_t ldy,
+                  void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes for int8_gemm (0 if the shape is invalid). */
+size_t tg_int8_workspace_size(int32_t M, int32_t m, int32_t n);
+
+/*
+ * The experts' products over routed pairs (moe_group's order and offsets), in one launch:
+ *     Y[p, o] = (sum_i xq[t, i] * wq[e, o, i]) * xs[t] * wscales[e, o],  t = p / pairs_per_row,
+ * for every pair p = order[j] of expert e, offsets[e] <= j < offsets[e + 1]. Rows of Y whose pair belongs
+ * to no expert are left as they were. pairs_per_row = top_k reads one activation row for all experts of a
+ * token (gate and up); 1 reads a row for each pair (down).
+ *   pairs : 1 .. 2^20, a multiple of pairs_per_row; experts : 1 .. 1024; m, n : as for int8_gemm.
+ *   xq    : device, pairs / pairs_per_row rows, as for int8_gemm; xs : device, as many fp32.
+ *   wq    : device, experts * m contiguous rows of n int8, 16-byte aligned; wscales : device, experts * m fp32.
+ *   Y     : device, pairs rows, as for int8_gemm.
+ * Offsets are cut to [0, pairs] and entries of order outside [0, pairs) are skipped; a pair listed twice
+ * for different experts leaves either's product.
+ */
+int32_t int8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int32_t n, const int8_t *xq, int64_t ldx,
+                          const float *xs, int32_t pairs_per_row, const int8_t *wq, const float *wscales,
+                          const int32_t *offsets, const int32_t *order, void *Y, int32_t out_dtype, int64_t ldy,
+                          void *stream);
+
 #ifdef __cplusplus
 }
 #endif

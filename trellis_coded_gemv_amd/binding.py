@@ -31,7 +31,11 @@ EXPORTS = ("tg_abi_version", "tg_build_id", "tg_workspace_status", "tg_status_st
            "tg_decode_ceiling",
            "rht_apply", "trellis_gemv_grouped", "tg_grouped_workspace_size", "trellis_decode", "tg_code_table",
            "trellis_encode", "tg_encode_workspace_size", "trellis_gemm_prefill", "tg_prefill_workspace_size",
-           "trellis_moe_block", "tg_moe_workspace_size")
+           "trellis_moe_block", "tg_moe_workspace_size",
+           "moe_route", "moe_group", "int8_quantize", "int8_gemm", "tg_int8_workspace_size", "int8_gemm_grouped")
+
+TG_ROUTE_SIGMOID = 1
+TG_ROUTE_RENORM = 2
 
 
 class TgLayer(ctypes.Structure):
@@ -93,6 +97,12 @@ def lib() -> ctypes.CDLL:
         "tg_prefill_workspace_size": (SZ, [LP, I32]),
         "trellis_moe_block": (I32, [LP, P, I32, LP, P, I32, P, P, I32, P, P, P, SZ, P]),
         "tg_moe_workspace_size": (SZ, [LP, I32, LP, I32, I32]),
+        "moe_route": (I32, [I32, I32, I32, P, I32, I64, P, I32, I32, I32, I32, ctypes.c_float, P, P, P]),
+        "moe_group": (I32, [I32, I32, P, P, P, P]),
+        "int8_quantize": (I32, [I32, I32, P, I32, I64, P, I64, P, P]),
+        "int8_gemm": (I32, [I32, I32, I32, P, I64, P, P, I64, P, P, I32, I64, P, SZ, P]),
+        "tg_int8_workspace_size": (SZ, [I32, I32, I32]),
+        "int8_gemm_grouped": (I32, [I32, I32, I32, I32, P, I64, P, I32, P, P, P, P, P, I32, I64, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -385,6 +395,262 @@ def trellis_moe_block(gate_up: "LayerTable", down: "LayerTable", sel, weights, x
                                    len(down), _ptr(sel), _ptr(weights), top_k, _ptr(x), _ptr(y), _ptr(ws),
                                    ws.numel(), _stream(stream)), "trellis_moe_block")
     return y
+
+
+# ---- routing and 8-bit products ------------------------------------------------------------
+# These entry points look at every tensor they are given: the data type, the shape, the innermost
+# stride and the device, so that nothing of the wrong layout reaches a kernel. The work runs on the
+# tensors' own device: on `stream`, or on that device's current stream.
+
+_DTYPES = {}
+
+
+def _dtype_code(dtype, where: str) -> int:
+    if not _DTYPES:
+        torch = _torch()
+        _DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"{where}: expected float32, float16 or bfloat16, got {dtype}")
+    return code
+
+
+def _expect(ok: bool, where: str, what: str) -> None:
+    if not ok:
+        raise ValueError(f"{where}: {what}")
+
+
+def _on_device(where: str, first, *others):
+    """The common device of the tensors (None among them is skipped)."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"{where}: expected tensors on a GPU, got {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{where}: tensors on {dev} and {t.device}")
+    return dev
+
+
+class _Launch:
+    """The device and stream of a call. Entered, they are current, so that what the call allocates belongs to its stream."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        self.raw, self._enter = None, []
+        if stream is None:
+            if device.index != torch.cuda.current_device():
+                self._enter.append(torch.cuda.device(device))
+            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.raw = stream.cuda_stream
+            self._enter += [torch.cuda.device(device), torch.cuda.stream(stream)]
+
+    def __enter__(self):
+        for c in self._enter:
+            c.__enter__()
+        return self.raw
+
+    def __exit__(self, *exc):
+        for c in reversed(self._enter):
+            c.__exit__(*exc)
+
+
+def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int = 1, topk_group: int = 1,
+              group_top: int = 1, renormalize: bool = True, scale: float = 1.0, sel=None, weights=None, stream=None):
+    """Expert ids int32 [tokens, top_k] and weights fp32 [tokens, top_k] of router logits [tokens, experts] (fp32, fp16 or
+    bf16): scores by softmax or sigmoid, selection by score + bias within the best topk_group of n_group groups (a group's
+    value: its group_top largest, summed), weights from the scores alone. Ids of slots without an expert are -1, weight 0."""
+    torch = _torch()
+    w = "moe_route"
+    _expect(logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1), w, "expected logits [tokens, experts] with neighbouring experts")
+    tokens, experts = logits.shape
+    dtype = _dtype_code(logits.dtype, w)
+    if bias is not None:
+        _expect(bias.dtype == torch.float32 and bias.shape == (experts,) and bias.is_contiguous(), w, f"expected a float32 bias [{experts}]")
+    dev = _on_device(w, logits, bias, sel, weights)
+    with _Launch(dev, stream) as s:
+        if sel is None:
+            sel = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
+        if weights is None:
+            weights = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
+        _expect(sel.dtype == torch.int32 and sel.shape == (tokens, top_k) and sel.is_contiguous(), w, f"expected sel int32 [{tokens}, {top_k}]")
+        _expect(weights.dtype == torch.float32 and weights.shape == (tokens, top_k) and weights.is_contiguous(), w,
+                f"expected weights float32 [{tokens}, {top_k}]")
+        flags = (TG_ROUTE_SIGMOID if sigmoid else 0) | (TG_ROUTE_RENORM if renormalize else 0)
+        _check(lib().moe_route(tokens, experts, top_k, logits.data_ptr(), dtype, logits.stride(0) if tokens > 1 else experts,
+                               _ptr(bias), n_group, topk_group, group_top, flags, scale, sel.data_ptr(), weights.data_ptr(), s), w)
+    return sel, weights
+
+
+def moe_group(sel, experts: int, offsets=None, order=None, stream=None):
+    """The routed pairs (token * top_k + slot) in expert order: offsets int32 [experts + 1] and order int32 [pairs], of
+    int32 ids of any shape; the pairs whose id is no expert come last, behind offsets[experts]."""
+    torch = _torch()
+    w = "moe_group"
+    _expect(sel.dtype == torch.int32 and sel.is_contiguous(), w, "expected contiguous int32 ids")
+    pairs = sel.numel()
+    dev = _on_device(w, sel, offsets, order)
+    with _Launch(dev, stream) as s:
+        if offsets is None:
+            offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
+        if order is None:
+            order = torch.empty(pairs, dtype=torch.int32, device=dev)
+        _expect(offsets.dtype == torch.int32 and offsets.shape == (experts + 1,) and offsets.is_contiguous(), w,
+                f"expected offsets int32 [{experts + 1}]")
+        _expect(order.dtype == torch.int32 and order.shape == (pairs,) and order.is_contiguous(), w, f"expected order int32 [{pairs}]")
+        _check(lib().moe_group(pairs, experts, sel.data_ptr(), offsets.data_ptr(), order.data_ptr(), s), w)
+    return offsets, order
+
+
+def int8_quantize(x, q=None, scales=None, stream=None):
+    """Rows x [..., n] (fp32, fp16 or bf16) as int8 [..., n] with a scale for each row (fp32 [...]): x is about q * scale."""
+    torch = _torch()
+    w = "int8_quantize"
+    _expect(x.dim() >= 1 and x.numel() > 0, w, "expected rows [..., n]")
+    lead, n = x.shape[:-1], x.shape[-1]
+    dtype = _dtype_code(x.dtype, w)
+    dev = _on_device(w, x, q, scales)
+    with _Launch(dev, stream) as s:
+        x2 = x if x.dim() == 2 else x.reshape(-1, n)
+        if x2.stride(1) != 1 and n > 1:
+            x2 = x2.contiguous()
+        rows = x2.shape[0]
+        if q is None:
+            q = torch.empty((*lead, n), dtype=torch.int8, device=dev)
+        if scales is None:
+            scales = torch.empty(lead, dtype=torch.float32, device=dev)
+        _expect(q.dtype == torch.int8 and q.shape == x.shape and (q.is_contiguous() or (q.dim() == 2 and q.stride(1) == 1 and q.stride(0) >= n)),
+                w, "expected q int8 in the shape of x, with neighbouring values")
+        _expect(scales.dtype == torch.float32 and scales.shape == lead and scales.is_contiguous(), w, "expected a float32 scale for each row")
+        _check(lib().int8_quantize(rows, n, x2.data_ptr(), dtype, x2.stride(0) if rows > 1 else n, q.data_ptr(),
+                                   q.stride(0) if q.dim() == 2 and rows > 1 else n, scales.data_ptr(), s), w)
+    return q, scales
+
+
+class Int8Layer:
+    """A linear layer kept at 8 bits: q int8 [m, n] with a scale for each output channel (fp32 [m])."""
+
+    def __init__(self, q, scales):
+        torch = _torch()
+        w = "Int8Layer"
+        _expect(q.dtype == torch.int8 and q.dim() == 2 and q.stride(1) == 1, w, "expected q int8 [m, n] with neighbouring inputs")
+        _expect(scales.dtype == torch.float32 and scales.shape == q.shape[:1] and scales.is_contiguous(), w, "expected float32 scales [m]")
+        self.device = _on_device(w, q, scales)
+        self.q, self.scales = q, scales
+        self.m, self.n = int(q.shape[0]), int(q.shape[1])
+        self.ldw = q.stride(0) if self.m > 1 else self.n
+
+    @classmethod
+    def from_dense(cls, weight, stream=None):
+        """The nearest 8-bit layer of a dense weight [m, n] (fp32, fp16 or bf16)."""
+        return cls(*int8_quantize(weight, stream=stream))
+
+
+class Int8Experts:
+    """The experts of a block, kept at 8 bits: q int8 [experts, m, n], scales fp32 [experts, m]."""
+
+    def __init__(self, q, scales):
+        torch = _torch()
+        w = "Int8Experts"
+        _expect(q.dtype == torch.int8 and q.dim() == 3 and q.is_contiguous(), w, "expected contiguous q int8 [experts, m, n]")
+        _expect(scales.dtype == torch.float32 and scales.shape == q.shape[:2] and scales.is_contiguous(), w, "expected float32 scales [experts, m]")
+        self.device = _on_device(w, q, scales)
+        self.q, self.scales = q, scales
+        self.experts, self.m, self.n = (int(v) for v in q.shape)
+
+    @classmethod
+    def from_dense(cls, weight, stream=None):
+        """The nearest 8-bit experts of dense weights [experts, m, n]."""
+        return cls(*int8_quantize(weight, stream=stream))
+
+
+def int8_workspace(layer: "Int8Layer", M: int):
+    """Zero-filled workspace for int8_gemm with up to M rows of this layer."""
+    torch = _torch()
+    size = int(lib().tg_int8_workspace_size(int(M), layer.m, layer.n))
+    if size == 0:
+        raise TgError(-2, "tg_int8_workspace_size")
+    return torch.zeros(size, dtype=torch.uint8, device=layer.device)
+
+
+def _int8_rows(where: str, n: int, xq, xs):
+    torch = _torch()
+    _expect(xq.dtype == torch.int8 and xq.dim() == 2 and xq.shape[1] == n and xq.stride(1) == 1, where, f"expected xq int8 [rows, {n}]")
+    _expect(xs.dtype == torch.float32 and xs.shape == xq.shape[:1] and xs.is_contiguous(), where, "expected a float32 scale for each row of xq")
+    return xq.shape[0], (xq.stride(0) if xq.shape[0] > 1 else n)
+
+
+def _int8_out(where: str, Y, rows: int, m: int, out_dtype, dev):
+    torch = _torch()
+    if Y is None:
+        Y = torch.empty((rows, m), dtype=out_dtype or torch.float32, device=dev)
+    code = _dtype_code(Y.dtype, where)
+    _expect(out_dtype is None or out_dtype == Y.dtype, where, "Y is not of out_dtype")
+    _expect(Y.shape == (rows, m) and (Y.stride(1) == 1 or m == 1) and (rows == 1 or Y.stride(0) >= m), where, f"expected Y [{rows}, {m}] with neighbouring outputs")
+    return Y, code, (Y.stride(0) if rows > 1 else m)
+
+
+def int8_gemm(layer: "Int8Layer", xq, xs, Y=None, out_dtype=None, ws=None, stream=None):
+    """Y [M, m] = (xq wq^T) * xs[r] * scales[o] of 8-bit rows xq [M, n] with scales xs [M]; out_dtype (or Y's type) float32,
+    float16 or bfloat16."""
+    w = "int8_gemm"
+    M, ldx = _int8_rows(w, layer.n, xq, xs)
+    dev = _on_device(w, xq, xs, layer.q, Y, ws)
+    with _Launch(dev, stream) as s:
+        Y, code, ldy = _int8_out(w, Y, M, layer.m, out_dtype, dev)
+        if ws is None:
+            ws = int8_workspace(layer, M)
+        _check(lib().int8_gemm(M, layer.m, layer.n, xq.data_ptr(), ldx, xs.data_ptr(), layer.q.data_ptr(), layer.ldw,
+                               layer.scales.data_ptr(), Y.data_ptr(), code, ldy, ws.data_ptr(), ws.numel() * ws.element_size(), s), w)
+    return Y
+
+
+def int8_gemm_grouped(experts: "Int8Experts", xq, xs, offsets, order, pairs_per_row: int = 1, Y=None, out_dtype=None, stream=None):
+    """Y [pairs, m]: row p = order[j], offsets[e] <= j < offsets[e + 1], is expert e's product with the 8-bit row
+    xq[p // pairs_per_row]. Rows of pairs without an expert are left as they were."""
+    torch = _torch()
+    w = "int8_gemm_grouped"
+    rows, ldx = _int8_rows(w, experts.n, xq, xs)
+    pairs = rows * int(pairs_per_row)
+    _expect(order.dtype == torch.int32 and order.shape == (pairs,) and order.is_contiguous(), w, f"expected order int32 [{pairs}]")
+    _expect(offsets.dtype == torch.int32 and offsets.shape == (experts.experts + 1,) and offsets.is_contiguous(), w,
+            f"expected offsets int32 [{experts.experts + 1}]")
+    dev = _on_device(w, xq, xs, experts.q, offsets, order, Y)
+    with _Launch(dev, stream) as s:
+        Y, code, ldy = _int8_out(w, Y, pairs, experts.m, out_dtype, dev)
+        _check(lib().int8_gemm_grouped(pairs, experts.experts, experts.m, experts.n, xq.data_ptr(), ldx, xs.data_ptr(), int(pairs_per_row),
+                                       experts.q.data_ptr(), experts.scales.data_ptr(), offsets.data_ptr(), order.data_ptr(),
+                                       Y.data_ptr(), code, ldy, s), w)
+    return Y
+
+
+class Int8Linear:
+    """An 8-bit linear layer used like a dense one, beside TrellisLinear: y = W x over the last axis.
+
+    `forward(x)` takes fp32, fp16 or bf16 activations [..., n] on the device, quantises each row with a scale of its own
+    (int8_quantize) and returns fp32 [..., m] (int8_gemm). The workspace is kept and grows with the row count; calls are
+    ordered on one stream.
+    """
+
+    def __init__(self, layer: "Int8Layer"):
+        self.layer = layer
+        self._ws = None
+
+    def forward(self, x, stream=None):
+        n, m = self.layer.n, self.layer.m
+        _expect(x.shape[-1] == n, "Int8Linear", f"expected activations [..., {n}], got {tuple(x.shape)}")
+        xq, xs = int8_quantize(x, stream=stream)
+        xq, xs = xq.view(-1, n), xs.view(-1)
+        need = int(lib().tg_int8_workspace_size(xq.shape[0], m, n))
+        if self._ws is None or self._ws.numel() < need:
+            with _Launch(self.layer.device, stream):
+                self._ws = int8_workspace(self.layer, xq.shape[0])
+        y = int8_gemm(self.layer, xq, xs, ws=self._ws, stream=stream)
+        return y.reshape(x.shape[:-1] + (m,))
+
+    __call__ = forward
 
 
 class TrellisLinear:

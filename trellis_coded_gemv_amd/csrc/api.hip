@@ -732,3 +732,147 @@ TG_API int32_t trellis_moe_block(const tg_layer* gate_up, const tg_layer* d_gate
   if (launch_grouped(g2, w.dn.max_m / kBlock, w.dn.max_n, s) != hipSuccess) return TG_ERR_LAUNCH;
   return launch_status(launch_moe_combine(Y2, w.hidden, d_sel, d_weights, top_k, n_down, w.hidden, y, s));
 }
+
+namespace {
+
+bool bad_type(int32_t dtype) { return dtype < TG_F32 || dtype > TG_BF16; }
+
+size_t type_size(int32_t dtype) { return dtype == TG_F32 ? 4 : 2; }
+
+// 128 * 128 * n < 2^31: no sum of 8-bit products leaves int32.
+constexpr int32_t kInt8MaxN = 131056;
+
+int32_t check_int8_shape(int32_t rows, int32_t m, int32_t n) {
+  if (rows < 1 || rows > (1 << 20) || m < 1 || m > (1 << 22) || n < 16 || n % 16 != 0 || n > kInt8MaxN)
+    return TG_ERR_SHAPE;
+  return TG_OK;
+}
+
+// The operands that a dense product and the experts' share, after the shape has been checked.
+int32_t check_int8_operands(const Int8Args& a) {
+  if (!a.x || !a.xs || !a.w || !a.ws || !a.y) return TG_ERR_NULL;
+  if (bad_type(a.out) || a.ldx < a.n || a.ldx % 16 != 0 || a.ldw < a.n || a.ldw % 16 != 0 || a.ldy < a.m)
+    return TG_ERR_ARG;
+  if (misaligned(a.x, 16) || misaligned(a.w, 16) || misaligned(a.xs, 4) || misaligned(a.ws, 4) ||
+      misaligned(a.y, type_size(a.out)))
+    return TG_ERR_ALIGN;
+  return TG_OK;
+}
+
+int32_t wide_rows(const Int8Args& a) { return a.ldy % 4 == 0 && !misaligned(a.y, 4 * type_size(a.out)); }
+
+size_t int8_ws_bytes(int32_t, int32_t, int32_t) { return kWsHeader; }
+
+}  // namespace
+
+TG_API int32_t moe_route(int32_t tokens, int32_t experts, int32_t top_k, const void* logits, int32_t dtype, int64_t ld,
+                         const float* bias, int32_t n_group, int32_t topk_group, int32_t group_top, int32_t flags,
+                         float scale, int32_t* sel, float* weights, void* stream) {
+  if (tokens < 1 || tokens > (1 << 24) || experts < 1 || experts > kRouteMaxExperts) return TG_ERR_SHAPE;
+  if (top_k < 1 || top_k > kRouteMaxTopK || top_k > experts || bad_type(dtype) || ld < experts) return TG_ERR_ARG;
+  if (n_group < 1 || n_group > 64 || experts % n_group != 0 || topk_group < 1 || topk_group > n_group ||
+      topk_group * (experts / n_group) < top_k || (group_top != 1 && group_top != 2))
+    return TG_ERR_ARG;
+  if ((flags & ~(TG_ROUTE_SIGMOID | TG_ROUTE_RENORM)) != 0 || !(scale - scale == 0.f)) return TG_ERR_ARG;
+  if (!logits || !sel || !weights) return TG_ERR_NULL;
+  if (misaligned(logits, type_size(dtype)) || misaligned(bias, 4) || misaligned(sel, 4) || misaligned(weights, 4))
+    return TG_ERR_ALIGN;
+  RouteArgs a;
+  a.logits = logits;
+  a.bias = bias;
+  a.sel = sel;
+  a.weights = weights;
+  a.ld = ld;
+  a.tokens = tokens;
+  a.experts = experts;
+  a.top_k = top_k;
+  a.n_group = n_group;
+  a.topk_group = topk_group;
+  a.group_top = group_top;
+  a.sigmoid = (flags & TG_ROUTE_SIGMOID) != 0;
+  a.renorm = (flags & TG_ROUTE_RENORM) != 0;
+  a.scale = scale;
+  return launch_status(launch_moe_route(a, dtype, (hipStream_t)stream));
+}
+
+TG_API int32_t moe_group(int32_t pairs, int32_t experts, const int32_t* sel, int32_t* offsets, int32_t* order,
+                         void* stream) {
+  if (pairs < 1 || pairs > (1 << 24) || experts < 1 || experts > kRouteMaxExperts) return TG_ERR_SHAPE;
+  if (!sel || !offsets || !order) return TG_ERR_NULL;
+  if (misaligned(sel, 4) || misaligned(offsets, 4) || misaligned(order, 4)) return TG_ERR_ALIGN;
+  return launch_status(launch_moe_group(pairs, experts, sel, offsets, order, (hipStream_t)stream));
+}
+
+TG_API int32_t int8_quantize(int32_t rows, int32_t n, const void* x, int32_t dtype, int64_t ldx, int8_t* q,
+                             int64_t ldq, float* scales, void* stream) {
+  if (rows < 1 || rows > (1 << 24) || n < 1 || n > (1 << 22)) return TG_ERR_SHAPE;
+  if (bad_type(dtype) || ldx < n || ldq < n) return TG_ERR_ARG;
+  if (!x || !q || !scales) return TG_ERR_NULL;
+  if (misaligned(x, type_size(dtype)) || misaligned(scales, 4)) return TG_ERR_ALIGN;
+  return launch_status(launch_int8_quantize(rows, n, x, dtype, ldx, q, ldq, scales, (hipStream_t)stream));
+}
+
+TG_API size_t tg_int8_workspace_size(int32_t M, int32_t m, int32_t n) {
+  return check_int8_shape(M, m, n) == TG_OK ? int8_ws_bytes(M, m, n) : 0;
+}
+
+TG_API int32_t int8_gemm(int32_t M, int32_t m, int32_t n, const int8_t* xq, int64_t ldx, const float* xs,
+                         const int8_t* wq, int64_t ldw, const float* wscales, void* Y, int32_t out_dtype, int64_t ldy,
+                         void* ws, size_t ws_bytes, void* stream) {
+  int32_t st = check_int8_shape(M, m, n);
+  if (st != TG_OK) return st;
+  Int8Args a{};
+  a.x = xq;
+  a.xs = xs;
+  a.w = wq;
+  a.ws = wscales;
+  a.y = Y;
+  a.ldx = ldx;
+  a.ldw = ldw;
+  a.ldy = ldy;
+  a.M = M;
+  a.m = m;
+  a.n = n;
+  a.experts = 1;
+  a.pairs_per_row = 1;
+  a.out = out_dtype;
+  st = check_int8_operands(a);
+  if (st != TG_OK) return st;
+  if (!ws || ws_bytes < int8_ws_bytes(M, m, n)) return TG_ERR_WORKSPACE;
+  if (misaligned(ws, kAlign)) return TG_ERR_ALIGN;
+  a.wide_y = wide_rows(a);
+  return launch_status(launch_int8_gemm(a, (hipStream_t)stream));
+}
+
+TG_API int32_t int8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int32_t n, const int8_t* xq, int64_t ldx,
+                                 const float* xs, int32_t pairs_per_row, const int8_t* wq, const float* wscales,
+                                 const int32_t* offsets, const int32_t* order, void* Y, int32_t out_dtype, int64_t ldy,
+                                 void* stream) {
+  int32_t st = check_int8_shape(pairs, m, n);
+  if (st != TG_OK) return st;
+  if (experts < 1 || experts > kRouteMaxExperts) return TG_ERR_SHAPE;
+  if (pairs_per_row < 1 || pairs % pairs_per_row != 0) return TG_ERR_ARG;
+  Int8Args a{};
+  a.x = xq;
+  a.xs = xs;
+  a.w = wq;
+  a.ws = wscales;
+  a.offsets = offsets;
+  a.order = order;
+  a.y = Y;
+  a.ldx = ldx;
+  a.ldw = n;
+  a.ldy = ldy;
+  a.M = pairs;
+  a.m = m;
+  a.n = n;
+  a.experts = experts;
+  a.pairs_per_row = pairs_per_row;
+  a.out = out_dtype;
+  st = check_int8_operands(a);
+  if (st != TG_OK) return st;
+  if (!offsets || !order) return TG_ERR_NULL;
+  if (misaligned(offsets, 4) || misaligned(order, 4)) return TG_ERR_ALIGN;
+  a.wide_y = wide_rows(a);
+  return launch_status(launch_int8_gemm(a, (hipStream_t)stream));
+}

@@ -125,6 +125,44 @@ hipError_t launch_prefill_rht(const uint16_t* X, int64_t ldx, const uint32_t* si
 hipError_t launch_prefill_mfma(const uint32_t* codes, const uint16_t* scales, const uint32_t* sign_out,
                                const uint16_t* Xt, float* Y, int64_t ldy, int m, int n, int M, int k_bits, int code_id,
                                hipStream_t s);
+
+// Element types of the routing and 8-bit entry points (TG_F32, TG_F16, TG_BF16).
+constexpr int kF32 = 0, kF16 = 1, kBf16 = 2;
+
+// Routing of tokens to experts (route.hip).
+constexpr int kRouteMaxExperts = 1024;   // 16 experts in each lane of a wave
+constexpr int kRouteMaxTopK = 64;        // one slot in each lane
+struct RouteArgs {
+  const void* logits;
+  const float* bias;      // or null
+  int32_t* sel;
+  float* weights;
+  int64_t ld;
+  int32_t tokens, experts, top_k, n_group, topk_group, group_top;
+  int32_t sigmoid, renorm;
+  float scale;
+};
+hipError_t launch_moe_route(const RouteArgs& a, int dtype, hipStream_t s);
+hipError_t launch_moe_group(int pairs, int experts, const int32_t* sel, int32_t* offsets, int32_t* order, hipStream_t s);
+
+// 8-bit products (int8.hip): dense, or the experts of routed pairs when offsets is set.
+struct Int8Args {
+  const int8_t* x;
+  const float* xs;
+  const int8_t* w;        // [experts][m] rows
+  const float* ws;        // [experts][m]
+  const int32_t* offsets; // [experts + 1], or null: dense
+  const int32_t* order;   // [M] pairs in expert order
+  void* y;
+  int64_t ldx, ldw, ldy;
+  int32_t M, m, n;        // M: output rows (pairs)
+  int32_t experts, pairs_per_row;
+  int32_t out;            // kF32, kF16, kBf16
+  int32_t wide_y;         // four neighbouring outputs of a row can be stored at once
+};
+hipError_t launch_int8_quantize(int rows, int n, const void* x, int dtype, int64_t ldx, int8_t* q, int64_t ldq,
+                                float* scales, hipStream_t s);
+hipError_t launch_int8_gemm(const Int8Args& a, hipStream_t s);
 constexpr int kEncMaxSlots = 256;        // encoder workgroups in flight (one tile each at a time)
 
 // LDS bytes a GEMV workgroup needs for a chunk of `chunk_blocks` 128-blocks.

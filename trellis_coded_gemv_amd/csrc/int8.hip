@@ -4,12 +4,9 @@
 // The sums are exact in int32 (|q| <= 128 and n < 2^17, so no sum leaves the type), whatever the order and the
 // split of the work; one output is rounded three times in binary32 (the sum, and its product with either scale),
 // and once more to a 16-bit output type.
-#include "tg_device.hpp"
-#include "tg_internal.hpp"
+#include "tg_int8.hpp"
 
 namespace tg {
-
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
 // Quantiser: amax = max |x_i| of the row, scale = amax / 127, q_i = the whole number nearest to x_i * 127 / amax,
@@ -69,83 +66,6 @@ hipError_t launch_int8_quantize(int rows, int n, const void* x, int dtype, int64
 // lane ends with four neighbouring outputs of one activation row. Lane l supplies row l % 16 and the 16 bytes at
 // 16 * (l / 16) of a 64-byte step on both sides.
 // ---------------------------------------------------------------------------
-
-// Which activation rows a workgroup's row tile covers. Dense: rows [r0, r0 + R). Experts: the tiles of `rows_per_tile`
-// pairs are numbered expert by expert; every wave finds its tile's expert from the offsets (a wave holds up to 16
-// neighbouring experts in each lane).
-struct RowTile {
-  int expert, first, count;   // count 0: nothing to do
-};
-
-__device__ __forceinline__ RowTile find_tile(const Int8Args& a, int tile, int rows_per_tile) {
-  if (!a.offsets) {
-    const int first = tile * rows_per_tile;
-    return {0, first, min(rows_per_tile, a.M - first)};
-  }
-  const int lane = threadIdx.x & 63;
-  const int per = (a.experts + 63) >> 6;
-  const int e0 = lane * per;
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int e = e0 + i;
-    if (e < a.experts) {
-      const int b = min(max(a.offsets[e], 0), a.M), c = min(max(a.offsets[e + 1], 0), a.M);
-      mine += c > b ? (c - b + rows_per_tile - 1) / rows_per_tile : 0;
-    }
-  }
-  int upto = mine;
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(upto, d, 64);
-    if (lane >= d) upto += v;
-  }
-  RowTile t{0, 0, 0};
-  const uint64_t has = __ballot(upto > tile);
-  if (has == 0) return t;
-  const int owner = __builtin_ctzll(has);
-  int left = tile - __shfl(upto - mine, owner, 64);
-  for (int i = 0; i < per; ++i) {
-    const int e = owner * per + i;
-    if (e >= a.experts) break;
-    const int b = min(max(a.offsets[e], 0), a.M), c = min(max(a.offsets[e + 1], 0), a.M);
-    const int nt = c > b ? (c - b + rows_per_tile - 1) / rows_per_tile : 0;
-    if (left < nt) {
-      t.expert = e;
-      t.first = b + left * rows_per_tile;
-      t.count = min(rows_per_tile, c - t.first);
-      return t;
-    }
-    left -= nt;
-  }
-  return t;
-}
-
-// Pair (output row) of a tile's row, or -1; the activation row is pair / pairs_per_row.
-__device__ __forceinline__ int pair_of(const Int8Args& a, const RowTile& t, int i) {
-  if (i >= t.count) return -1;
-  if (!a.offsets) return t.first + i;
-  const int p = a.order[t.first + i];
-  return p >= 0 && p < a.M ? p : -1;
-}
-
-template <int DT>
-__device__ __forceinline__ void store4(void* y, int64_t at, const float (&v)[4], int valid, bool wide) {
-  if constexpr (DT == kF32) {
-    float* p = reinterpret_cast<float*>(y) + at;
-    if (valid >= 4 && wide) *reinterpret_cast<float4_t*>(p) = float4_t{v[0], v[1], v[2], v[3]};
-    else
-      for (int i = 0; i < 4; ++i)
-        if (i < valid) p[i] = v[i];
-  } else {
-    uint16_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = DT == kF16 ? __builtin_bit_cast(uint16_t, (_Float16)v[i]) : __builtin_bit_cast(uint16_t, (__bf16)v[i]);
-    uint16_t* p = reinterpret_cast<uint16_t*>(y) + at;
-    if (valid >= 4 && wide) *reinterpret_cast<u32x2*>(p) = u32x2{(uint32_t)h[0] | (uint32_t)h[1] << 16, (uint32_t)h[2] | (uint32_t)h[3] << 16};
-    else
-      for (int i = 0; i < 4; ++i)
-        if (i < valid) p[i] = h[i];
-  }
-}
 
 // A workgroup of 8 waves owns 16*OT outputs and 16*RT activation rows; its waves share out the inner axis in blocks
 // of 256 bytes and are summed through LDS at the end.
@@ -230,18 +150,11 @@ static hipError_t launch_rows(const Int8Args& a, int tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Row tiles of a launch: exact for a dense product; for the experts' an upper bound that holds for every way the
-// pairs can fall (each expert with pairs leaves at most one tile part-filled).
-static int row_tiles(const Int8Args& a, int rows_per_tile) {
-  const int full = (a.M + rows_per_tile - 1) / rows_per_tile;
-  if (!a.offsets) return full;
-  return a.M / rows_per_tile + (a.experts < a.M ? a.experts : a.M);
-}
-
 hipError_t launch_int8_gemm(const Int8Args& a, hipStream_t s) {
   const int avg = a.offsets ? (a.M + a.experts - 1) / a.experts : a.M;
   if (avg <= 16) return launch_rows<1, 1>(a, row_tiles(a, 16), s);
   if (avg <= 32) return launch_rows<2, 2>(a, row_tiles(a, 32), s);
+  if (avg > 128) return launch_int8_tile(a, s);
   return launch_rows<4, 2>(a, row_tiles(a, 64), s);
 }
 

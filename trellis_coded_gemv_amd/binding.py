@@ -398,9 +398,12 @@ def trellis_moe_block(gate_up: "LayerTable", down: "LayerTable", sel, weights, x
 
 
 # ---- routing and 8-bit products ------------------------------------------------------------
-# These entry points look at every tensor they are given: the data type, the shape, the innermost
-# stride and the device, so that nothing of the wrong layout reaches a kernel. The work runs on the
-# tensors' own device: on `stream`, or on that device's current stream.
+# These entry points look at every tensor they are given -- type, shape, innermost stride, device --
+# so that nothing of the wrong layout reaches a kernel. The work runs on the tensors' own device: on
+# `stream`, or on that device's current stream. Small calls take a few microseconds on the GPU, so
+# the common way through (no stream named, the tensors on the current device) is kept short; any
+# other call enters its device and stream and comes back on the common way, and what it allocates
+# belongs to that stream.
 
 _DTYPES = {}
 
@@ -420,41 +423,44 @@ def _expect(ok: bool, where: str, what: str) -> None:
         raise ValueError(f"{where}: {what}")
 
 
-def _on_device(where: str, first, *others):
-    """The common device of the tensors (None among them is skipped)."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"{where}: expected tensors on a GPU, got {dev}")
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{where}: tensors on {dev} and {t.device}")
-    return dev
+def _common_device(where: str, *tensors) -> int:
+    """Index of the GPU that holds every tensor (None among them is skipped)."""
+    at = tensors[0].get_device()
+    if at < 0:
+        raise ValueError(f"{where}: expected tensors on a GPU, got {tensors[0].device}")
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"{where}: tensors on {tensors[0].device} and {t.device}")
+    return at
 
 
-class _Launch:
-    """The device and stream of a call. Entered, they are current, so that what the call allocates belongs to its stream."""
+def _elsewhere(torch, at: int, stream) -> bool:
+    """Whether a call has to enter another device or stream than the current ones."""
+    return stream is not None or at != torch.cuda.current_device()
 
-    def __init__(self, device, stream):
+
+class _Entered:
+    """The device and stream of a call, as the current ones."""
+
+    def __init__(self, at: int, stream):
         torch = _torch()
-        self.raw, self._enter = None, []
-        if stream is None:
-            if device.index != torch.cuda.current_device():
-                self._enter.append(torch.cuda.device(device))
-            self.raw = torch._C._cuda_getCurrentRawStream(device.index)
-        else:
+        self._enter = [torch.cuda.device(at)]
+        if stream is not None:
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.raw = stream.cuda_stream
-            self._enter += [torch.cuda.device(device), torch.cuda.stream(stream)]
+                stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", at))
+            self._enter.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for c in self._enter:
             c.__enter__()
-        return self.raw
 
     def __exit__(self, *exc):
         for c in reversed(self._enter):
             c.__exit__(*exc)
+
+
+def _current(torch, at: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(at)
 
 
 def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int = 1, topk_group: int = 1,
@@ -464,23 +470,29 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int
     value: its group_top largest, summed), weights from the scores alone. Ids of slots without an expert are -1, weight 0."""
     torch = _torch()
     w = "moe_route"
-    _expect(logits.dim() == 2 and (logits.stride(1) == 1 or logits.shape[1] == 1), w, "expected logits [tokens, experts] with neighbouring experts")
-    tokens, experts = logits.shape
     dtype = _dtype_code(logits.dtype, w)
+    _expect(logits.dim() == 2, w, "expected logits [tokens, experts]")
+    tokens, experts = logits.shape
+    ld, inner = logits.stride()
+    _expect(inner == 1 or experts == 1, w, "a token's logits have to be neighbours")
     if bias is not None:
         _expect(bias.dtype == torch.float32 and bias.shape == (experts,) and bias.is_contiguous(), w, f"expected a float32 bias [{experts}]")
-    dev = _on_device(w, logits, bias, sel, weights)
-    with _Launch(dev, stream) as s:
-        if sel is None:
-            sel = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
-        if weights is None:
-            weights = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
+    at = _common_device(w, logits, bias, sel, weights)
+    if _elsewhere(torch, at, stream):
+        with _Entered(at, stream):
+            return moe_route(logits, top_k, bias, sigmoid, n_group, topk_group, group_top, renormalize, scale, sel, weights)
+    if sel is None:
+        sel = logits.new_empty((tokens, top_k), dtype=torch.int32)
+    else:
         _expect(sel.dtype == torch.int32 and sel.shape == (tokens, top_k) and sel.is_contiguous(), w, f"expected sel int32 [{tokens}, {top_k}]")
+    if weights is None:
+        weights = logits.new_empty((tokens, top_k), dtype=torch.float32)
+    else:
         _expect(weights.dtype == torch.float32 and weights.shape == (tokens, top_k) and weights.is_contiguous(), w,
                 f"expected weights float32 [{tokens}, {top_k}]")
-        flags = (TG_ROUTE_SIGMOID if sigmoid else 0) | (TG_ROUTE_RENORM if renormalize else 0)
-        _check(lib().moe_route(tokens, experts, top_k, logits.data_ptr(), dtype, logits.stride(0) if tokens > 1 else experts,
-                               _ptr(bias), n_group, topk_group, group_top, flags, scale, sel.data_ptr(), weights.data_ptr(), s), w)
+    flags = (TG_ROUTE_SIGMOID if sigmoid else 0) | (TG_ROUTE_RENORM if renormalize else 0)
+    _check(lib().moe_route(tokens, experts, top_k, logits.data_ptr(), dtype, ld if tokens > 1 else experts, None if bias is None else bias.data_ptr(),
+                           n_group, topk_group, group_top, flags, scale, sel.data_ptr(), weights.data_ptr(), _current(torch, at)), w)
     return sel, weights
 
 
@@ -491,16 +503,20 @@ def moe_group(sel, experts: int, offsets=None, order=None, stream=None):
     w = "moe_group"
     _expect(sel.dtype == torch.int32 and sel.is_contiguous(), w, "expected contiguous int32 ids")
     pairs = sel.numel()
-    dev = _on_device(w, sel, offsets, order)
-    with _Launch(dev, stream) as s:
-        if offsets is None:
-            offsets = torch.empty(experts + 1, dtype=torch.int32, device=dev)
-        if order is None:
-            order = torch.empty(pairs, dtype=torch.int32, device=dev)
+    at = _common_device(w, sel, offsets, order)
+    if _elsewhere(torch, at, stream):
+        with _Entered(at, stream):
+            return moe_group(sel, experts, offsets, order)
+    if offsets is None:
+        offsets = sel.new_empty(experts + 1)
+    else:
         _expect(offsets.dtype == torch.int32 and offsets.shape == (experts + 1,) and offsets.is_contiguous(), w,
                 f"expected offsets int32 [{experts + 1}]")
+    if order is None:
+        order = sel.new_empty(pairs)
+    else:
         _expect(order.dtype == torch.int32 and order.shape == (pairs,) and order.is_contiguous(), w, f"expected order int32 [{pairs}]")
-        _check(lib().moe_group(pairs, experts, sel.data_ptr(), offsets.data_ptr(), order.data_ptr(), s), w)
+    _check(lib().moe_group(pairs, experts, sel.data_ptr(), offsets.data_ptr(), order.data_ptr(), _current(torch, at)), w)
     return offsets, order
 
 
@@ -508,24 +524,33 @@ def int8_quantize(x, q=None, scales=None, stream=None):
     """Rows x [..., n] (fp32, fp16 or bf16) as int8 [..., n] with a scale for each row (fp32 [...]): x is about q * scale."""
     torch = _torch()
     w = "int8_quantize"
-    _expect(x.dim() >= 1 and x.numel() > 0, w, "expected rows [..., n]")
-    lead, n = x.shape[:-1], x.shape[-1]
     dtype = _dtype_code(x.dtype, w)
-    dev = _on_device(w, x, q, scales)
-    with _Launch(dev, stream) as s:
-        x2 = x if x.dim() == 2 else x.reshape(-1, n)
-        if x2.stride(1) != 1 and n > 1:
-            x2 = x2.contiguous()
-        rows = x2.shape[0]
-        if q is None:
-            q = torch.empty((*lead, n), dtype=torch.int8, device=dev)
-        if scales is None:
-            scales = torch.empty(lead, dtype=torch.float32, device=dev)
-        _expect(q.dtype == torch.int8 and q.shape == x.shape and (q.is_contiguous() or (q.dim() == 2 and q.stride(1) == 1 and q.stride(0) >= n)),
+    shape = x.shape
+    _expect(len(shape) >= 1 and x.numel() > 0, w, "expected rows [..., n]")
+    at = _common_device(w, x, q, scales)
+    if _elsewhere(torch, at, stream):
+        with _Entered(at, stream):
+            return int8_quantize(x, q, scales)
+    lead, n = shape[:-1], shape[-1]
+    x2 = x if len(shape) == 2 else x.reshape(-1, n)
+    ldx, inner = x2.stride()
+    if inner != 1 and n > 1:
+        x2 = x2.contiguous()
+        ldx = n
+    rows, ldq = x2.shape[0], n
+    if q is None:
+        q = x2.new_empty(shape, dtype=torch.int8)
+    else:
+        _expect(q.dtype == torch.int8 and q.shape == shape and (q.is_contiguous() or (q.dim() == 2 and q.stride(1) == 1 and q.stride(0) >= n)),
                 w, "expected q int8 in the shape of x, with neighbouring values")
+        if q.dim() == 2 and rows > 1:
+            ldq = q.stride(0)
+    if scales is None:
+        scales = x2.new_empty(lead, dtype=torch.float32)
+    else:
         _expect(scales.dtype == torch.float32 and scales.shape == lead and scales.is_contiguous(), w, "expected a float32 scale for each row")
-        _check(lib().int8_quantize(rows, n, x2.data_ptr(), dtype, x2.stride(0) if rows > 1 else n, q.data_ptr(),
-                                   q.stride(0) if q.dim() == 2 and rows > 1 else n, scales.data_ptr(), s), w)
+    _check(lib().int8_quantize(rows, n, x2.data_ptr(), dtype, ldx if rows > 1 else n, q.data_ptr(), ldq, scales.data_ptr(),
+                               _current(torch, at)), w)
     return q, scales
 
 
@@ -537,8 +562,8 @@ class Int8Layer:
         w = "Int8Layer"
         _expect(q.dtype == torch.int8 and q.dim() == 2 and q.stride(1) == 1, w, "expected q int8 [m, n] with neighbouring inputs")
         _expect(scales.dtype == torch.float32 and scales.shape == q.shape[:1] and scales.is_contiguous(), w, "expected float32 scales [m]")
-        self.device = _on_device(w, q, scales)
-        self.q, self.scales = q, scales
+        _common_device(w, q, scales)
+        self.q, self.scales, self.device = q, scales, q.device
         self.m, self.n = int(q.shape[0]), int(q.shape[1])
         self.ldw = q.stride(0) if self.m > 1 else self.n
 
@@ -556,8 +581,8 @@ class Int8Experts:
         w = "Int8Experts"
         _expect(q.dtype == torch.int8 and q.dim() == 3 and q.is_contiguous(), w, "expected contiguous q int8 [experts, m, n]")
         _expect(scales.dtype == torch.float32 and scales.shape == q.shape[:2] and scales.is_contiguous(), w, "expected float32 scales [experts, m]")
-        self.device = _on_device(w, q, scales)
-        self.q, self.scales = q, scales
+        _common_device(w, q, scales)
+        self.q, self.scales, self.device = q, scales, q.device
         self.experts, self.m, self.n = (int(v) for v in q.shape)
 
     @classmethod
@@ -567,7 +592,7 @@ class Int8Experts:
 
 
 def int8_workspace(layer: "Int8Layer", M: int):
-    """Zero-filled workspace for int8_gemm with up to M rows of this layer."""
+    """Zero-filled workspace for int8_gemm with M rows of this layer."""
     torch = _torch()
     size = int(lib().tg_int8_workspace_size(int(M), layer.m, layer.n))
     if size == 0:
@@ -575,17 +600,20 @@ def int8_workspace(layer: "Int8Layer", M: int):
     return torch.zeros(size, dtype=torch.uint8, device=layer.device)
 
 
-def _int8_rows(where: str, n: int, xq, xs):
-    torch = _torch()
-    _expect(xq.dtype == torch.int8 and xq.dim() == 2 and xq.shape[1] == n and xq.stride(1) == 1, where, f"expected xq int8 [rows, {n}]")
-    _expect(xs.dtype == torch.float32 and xs.shape == xq.shape[:1] and xs.is_contiguous(), where, "expected a float32 scale for each row of xq")
-    return xq.shape[0], (xq.stride(0) if xq.shape[0] > 1 else n)
+def _int8_rows(torch, where: str, n: int, xq, xs):
+    _expect(xq.dtype == torch.int8 and xq.dim() == 2, where, f"expected xq int8 [rows, {n}]")
+    rows, width = xq.shape
+    ldx, inner = xq.stride()
+    _expect(width == n and inner == 1, where, f"expected xq int8 [rows, {n}] with neighbouring values")
+    _expect(xs.dtype == torch.float32 and xs.shape == (rows,) and xs.is_contiguous(), where, "expected a float32 scale for each row of xq")
+    return rows, (ldx if rows > 1 else n)
 
 
-def _int8_out(where: str, Y, rows: int, m: int, out_dtype, dev):
-    torch = _torch()
+def _int8_out(torch, where: str, Y, rows: int, m: int, out_dtype, xq):
     if Y is None:
-        Y = torch.empty((rows, m), dtype=out_dtype or torch.float32, device=dev)
+        dtype = torch.float32 if out_dtype is None else out_dtype
+        code = _dtype_code(dtype, where)
+        return xq.new_empty((rows, m), dtype=dtype), code, m
     code = _dtype_code(Y.dtype, where)
     _expect(out_dtype is None or out_dtype == Y.dtype, where, "Y is not of out_dtype")
     _expect(Y.shape == (rows, m) and (Y.stride(1) == 1 or m == 1) and (rows == 1 or Y.stride(0) >= m), where, f"expected Y [{rows}, {m}] with neighbouring outputs")
@@ -595,34 +623,40 @@ def _int8_out(where: str, Y, rows: int, m: int, out_dtype, dev):
 def int8_gemm(layer: "Int8Layer", xq, xs, Y=None, out_dtype=None, ws=None, stream=None):
     """Y [M, m] = (xq wq^T) * xs[r] * scales[o] of 8-bit rows xq [M, n] with scales xs [M]; out_dtype (or Y's type) float32,
     float16 or bfloat16."""
+    torch = _torch()
     w = "int8_gemm"
-    M, ldx = _int8_rows(w, layer.n, xq, xs)
-    dev = _on_device(w, xq, xs, layer.q, Y, ws)
-    with _Launch(dev, stream) as s:
-        Y, code, ldy = _int8_out(w, Y, M, layer.m, out_dtype, dev)
-        if ws is None:
-            ws = int8_workspace(layer, M)
-        _check(lib().int8_gemm(M, layer.m, layer.n, xq.data_ptr(), ldx, xs.data_ptr(), layer.q.data_ptr(), layer.ldw,
-                               layer.scales.data_ptr(), Y.data_ptr(), code, ldy, ws.data_ptr(), ws.numel() * ws.element_size(), s), w)
+    m, n = layer.m, layer.n
+    M, ldx = _int8_rows(torch, w, n, xq, xs)
+    at = _common_device(w, xq, xs, layer.q, Y, ws)
+    if _elsewhere(torch, at, stream):
+        with _Entered(at, stream):
+            return int8_gemm(layer, xq, xs, Y, out_dtype, ws)
+    Y, code, ldy = _int8_out(torch, w, Y, M, m, out_dtype, xq)
+    if ws is None:
+        ws = int8_workspace(layer, M)
+    _check(lib().int8_gemm(M, m, n, xq.data_ptr(), ldx, xs.data_ptr(), layer.q.data_ptr(), layer.ldw, layer.scales.data_ptr(),
+                           Y.data_ptr(), code, ldy, ws.data_ptr(), ws.numel() * ws.element_size(), _current(torch, at)), w)
     return Y
 
 
 def int8_gemm_grouped(experts: "Int8Experts", xq, xs, offsets, order, pairs_per_row: int = 1, Y=None, out_dtype=None, stream=None):
     """Y [pairs, m]: row p = order[j], offsets[e] <= j < offsets[e + 1], is expert e's product with the 8-bit row
-    xq[p // pairs_per_row]. Rows of pairs without an expert are left as they were."""
+    xq[p // pairs_per_row]. Rows of pairs without an expert are left as they were: pass a zeroed Y where there are any."""
     torch = _torch()
     w = "int8_gemm_grouped"
-    rows, ldx = _int8_rows(w, experts.n, xq, xs)
+    m, n, count = experts.m, experts.n, experts.experts
+    rows, ldx = _int8_rows(torch, w, n, xq, xs)
     pairs = rows * int(pairs_per_row)
     _expect(order.dtype == torch.int32 and order.shape == (pairs,) and order.is_contiguous(), w, f"expected order int32 [{pairs}]")
-    _expect(offsets.dtype == torch.int32 and offsets.shape == (experts.experts + 1,) and offsets.is_contiguous(), w,
-            f"expected offsets int32 [{experts.experts + 1}]")
-    dev = _on_device(w, xq, xs, experts.q, offsets, order, Y)
-    with _Launch(dev, stream) as s:
-        Y, code, ldy = _int8_out(w, Y, pairs, experts.m, out_dtype, dev)
-        _check(lib().int8_gemm_grouped(pairs, experts.experts, experts.m, experts.n, xq.data_ptr(), ldx, xs.data_ptr(), int(pairs_per_row),
-                                       experts.q.data_ptr(), experts.scales.data_ptr(), offsets.data_ptr(), order.data_ptr(),
-                                       Y.data_ptr(), code, ldy, s), w)
+    _expect(offsets.dtype == torch.int32 and offsets.shape == (count + 1,) and offsets.is_contiguous(), w, f"expected offsets int32 [{count + 1}]")
+    at = _common_device(w, xq, xs, experts.q, offsets, order, Y)
+    if _elsewhere(torch, at, stream):
+        with _Entered(at, stream):
+            return int8_gemm_grouped(experts, xq, xs, offsets, order, pairs_per_row, Y, out_dtype)
+    Y, code, ldy = _int8_out(torch, w, Y, pairs, m, out_dtype, xq)
+    _check(lib().int8_gemm_grouped(pairs, count, m, n, xq.data_ptr(), ldx, xs.data_ptr(), int(pairs_per_row), experts.q.data_ptr(),
+                                   experts.scales.data_ptr(), offsets.data_ptr(), order.data_ptr(), Y.data_ptr(), code, ldy,
+                                   _current(torch, at)), w)
     return Y
 
 
@@ -630,25 +664,26 @@ class Int8Linear:
     """An 8-bit linear layer used like a dense one, beside TrellisLinear: y = W x over the last axis.
 
     `forward(x)` takes fp32, fp16 or bf16 activations [..., n] on the device, quantises each row with a scale of its own
-    (int8_quantize) and returns fp32 [..., m] (int8_gemm). The workspace is kept and grows with the row count; calls are
-    ordered on one stream.
+    (int8_quantize) and returns fp32 [..., m] (int8_gemm). The workspace is kept and replaced by a larger one when a row
+    count needs it (the earlier ones live on, for graphs that were captured with them); calls are ordered on one stream.
     """
 
     def __init__(self, layer: "Int8Layer"):
         self.layer = layer
-        self._ws = None
+        self._ws, self._earlier = None, []
 
     def forward(self, x, stream=None):
         n, m = self.layer.n, self.layer.m
         _expect(x.shape[-1] == n, "Int8Linear", f"expected activations [..., {n}], got {tuple(x.shape)}")
-        xq, xs = int8_quantize(x, stream=stream)
+        if _elsewhere(_torch(), _common_device("Int8Linear", x, self.layer.q), stream):
+            with _Entered(x.get_device(), stream):
+                return self.forward(x)
+        xq, xs = int8_quantize(x)
         xq, xs = xq.view(-1, n), xs.view(-1)
-        need = int(lib().tg_int8_workspace_size(xq.shape[0], m, n))
-        if self._ws is None or self._ws.numel() < need:
-            with _Launch(self.layer.device, stream):
-                self._ws = int8_workspace(self.layer, xq.shape[0])
-        y = int8_gemm(self.layer, xq, xs, ws=self._ws, stream=stream)
-        return y.reshape(x.shape[:-1] + (m,))
+        if self._ws is None or self._ws.numel() < lib().tg_int8_workspace_size(xq.shape[0], m, n):
+            self._earlier.append(self._ws)
+            self._ws = int8_workspace(self.layer, xq.shape[0])
+        return int8_gemm(self.layer, xq, xs, ws=self._ws).reshape(x.shape[:-1] + (m,))
 
     __call__ = forward
 

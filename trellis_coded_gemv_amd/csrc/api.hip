@@ -761,7 +761,11 @@ int32_t check_int8_operands(const Int8Args& a) {
 
 int32_t wide_rows(const Int8Args& a) { return a.ldy % 4 == 0 && !misaligned(a.y, 4 * type_size(a.out)); }
 
-size_t int8_ws_bytes(int32_t, int32_t, int32_t) { return kWsHeader; }
+// The header, a counter for each tile of a product whose inner axis is split, and the parts' sums. The counters lie
+// at one place for every product and are zero between calls; the sums hold anything.
+size_t int8_ws_bytes(int32_t M, int32_t m, int32_t n) {
+  return round_up(kInt8Partials + int8_partial_bytes(M, m, n), kAlign);
+}
 
 }  // namespace
 
@@ -841,6 +845,8 @@ TG_API int32_t int8_gemm(int32_t M, int32_t m, int32_t n, const int8_t* xq, int6
   if (!ws || ws_bytes < int8_ws_bytes(M, m, n)) return TG_ERR_WORKSPACE;
   if (misaligned(ws, kAlign)) return TG_ERR_ALIGN;
   a.wide_y = wide_rows(a);
+  a.counters = reinterpret_cast<uint32_t*>((char*)ws + kWsHeader);
+  a.partials = reinterpret_cast<uint64_t*>((char*)ws + kInt8Partials);
   return launch_status(launch_int8_gemm(a, (hipStream_t)stream));
 }
 

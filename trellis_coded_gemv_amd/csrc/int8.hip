@@ -30,35 +30,152 @@ __device__ __forceinline__ int quantize_step(float x, double inv) {
   return (int)__builtin_bit_cast(uint64_t, s + whole);     // the low word of the sum is the whole number
 }
 
-template <int DT>
-__global__ __launch_bounds__(256) void quantize_kernel(const void* __restrict__ x, int64_t ldx, int8_t* __restrict__ q,
-                                                       int64_t ldq, float* __restrict__ scales, int n) {
-  __shared__ uint32_t wmax[4];
+// max |x| of a row over its workgroup, as the bits of a binary32 (NaN and infinity come out on top of every number).
+template <int THREADS>
+__device__ __forceinline__ uint32_t row_max(uint32_t top, uint32_t* sh) {
+  for (int m = 32; m; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, 64));
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w) top = max(top, sh[w]);
+  return top;
+}
+
+// The row's scale, and 127 / amax for its steps. Not finite: scale NaN, and `finite` false.
+struct RowScale {
+  double inv;
+  bool finite;
+};
+
+__device__ __forceinline__ RowScale row_scale(uint32_t top, float* scale) {
+  const float amax = __builtin_bit_cast(float, top);
+  RowScale r;
+  r.finite = top < 0x7F800000u;
+  r.inv = r.finite && top != 0 ? 127.0 / (double)amax : 0.0;
+  if (threadIdx.x == 0) *scale = r.finite ? amax / 127.0f : __builtin_nanf("");
+  return r;
+}
+
+// Rows whose 16-byte pieces are aligned: the row stays in registers between the two passes, PER pieces to a thread,
+// and is read once.
+template <int DT, int THREADS, int PER>
+__global__ __launch_bounds__(THREADS) void quantize_rows_kernel(const void* __restrict__ x, int64_t ldx,
+                                                                int8_t* __restrict__ q, int64_t ldq,
+                                                                float* __restrict__ scales, int n) {
+  constexpr int VEC = DT == kF32 ? 4 : 8;
+  __shared__ uint32_t wmax[THREADS / 64];
   const int row = blockIdx.x;
   const int64_t base = (int64_t)row * ldx;
-  uint32_t top = 0;                                        // max of |x| as bits: NaN and infinity come out on top
-  for (int i = threadIdx.x; i < n; i += 256)
-    top = max(top, __builtin_bit_cast(uint32_t, load_elem<DT>(x, base + i)) & 0x7FFFFFFFu);
-  for (int m = 32; m; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m, 64));
-  if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = top;
-  __syncthreads();
-  top = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
-  const float amax = __builtin_bit_cast(float, top);
-  const bool finite = top < 0x7F800000u;
-  if (threadIdx.x == 0) scales[row] = finite ? amax / 127.0f : __builtin_nanf("");
-  const double inv = finite && top != 0 ? 127.0 / (double)amax : 0.0;
+  const int pieces = n / VEC, rest = n - pieces * VEC;
+  u32x4 v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = threadIdx.x + THREADS * i;
+    v[i] = u32x4{0, 0, 0, 0};
+    if (c < pieces) {
+      if constexpr (DT == kF32) v[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(x) + base + c * VEC);
+      else v[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + base + c * VEC);
+    }
+  }
+  float last = 0.f;                                        // the row's end, short of a piece: one value to a thread
+  if ((int)threadIdx.x < rest) last = load_elem<DT>(x, base + pieces * VEC + threadIdx.x);
+  uint32_t top = 0;
+  if constexpr (DT == kF32) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) top = max(top, v[i][d] & 0x7FFFFFFFu);
+  } else {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    u16x2 t2 = {0, 0};
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        t2 = __builtin_elementwise_max(t2, __builtin_bit_cast(u16x2, v[i][d] & 0x7FFF7FFFu));
+    const uint16_t t1 = max(t2[0], t2[1]);
+    top = DT == kBf16 ? (uint32_t)t1 << 16 : __builtin_bit_cast(uint32_t, half_bits_to_float(t1));
+  }
+  top = max(top, __builtin_bit_cast(uint32_t, last) & 0x7FFFFFFFu);
+  const RowScale r = row_scale(row_max<THREADS>(top, wmax), scales + row);
   int8_t* qr = q + (int64_t)row * ldq;
-  for (int i = threadIdx.x; i < n; i += 256)
-    qr[i] = finite ? (int8_t)quantize_step(load_elem<DT>(x, base + i), inv) : (int8_t)0;
+  const uint32_t keep = r.finite ? ~0u : 0u;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int c = threadIdx.x + THREADS * i;
+    if (c >= pieces) break;
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < VEC / 4; ++h) {
+      int b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t word = DT == kF32 ? v[i][e] : v[i][2 * h + e / 2];
+        float f;
+        if constexpr (DT == kF32) f = __builtin_bit_cast(float, word);
+        else if constexpr (DT == kF16) f = half_bits_to_float((uint16_t)(word >> (16 * (e & 1))));
+        else f = __builtin_bit_cast(float, e & 1 ? word & 0xFFFF0000u : word << 16);
+        b[e] = quantize_step(f, r.inv);
+      }
+      w[h] = (((uint32_t)b[0] & 255u) | ((uint32_t)b[1] & 255u) << 8 | ((uint32_t)b[2] & 255u) << 16 | (uint32_t)b[3] << 24) & keep;
+    }
+    if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(qr + c * VEC) = w[0];
+    else *reinterpret_cast<u32x2*>(qr + c * VEC) = u32x2{w[0], w[1]};
+  }
+  if ((int)threadIdx.x < rest) qr[pieces * VEC + threadIdx.x] = r.finite ? (int8_t)quantize_step(last, r.inv) : (int8_t)0;
+}
+
+// Rows of any alignment and length, read twice.
+template <int DT, int THREADS>
+__global__ __launch_bounds__(THREADS) void quantize_any_kernel(const void* __restrict__ x, int64_t ldx,
+                                                               int8_t* __restrict__ q, int64_t ldq,
+                                                               float* __restrict__ scales, int n) {
+  __shared__ uint32_t wmax[THREADS / 64];
+  const int row = blockIdx.x;
+  const int64_t base = (int64_t)row * ldx;
+  uint32_t top = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += THREADS)
+    top = max(top, __builtin_bit_cast(uint32_t, load_elem<DT>(x, base + i)) & 0x7FFFFFFFu);
+  const RowScale r = row_scale(row_max<THREADS>(top, wmax), scales + row);
+  int8_t* qr = q + (int64_t)row * ldq;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += THREADS)
+    qr[i] = r.finite ? (int8_t)quantize_step(load_elem<DT>(x, base + i), r.inv) : (int8_t)0;
+}
+
+template <int DT, int THREADS>
+static void launch_quantize_rows(int rows, int n, const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scales,
+                                 hipStream_t s) {
+  constexpr int VEC = DT == kF32 ? 4 : 8;
+  const int per = (n / VEC + THREADS - 1) / THREADS;
+  const dim3 grid((unsigned)rows), block(THREADS);
+  if (per <= 1) hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 1>), grid, block, 0, s, x, ldx, q, ldq, scales, n);
+  else if (per <= 2) hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 2>), grid, block, 0, s, x, ldx, q, ldq, scales, n);
+  else if (per <= 4) hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 4>), grid, block, 0, s, x, ldx, q, ldq, scales, n);
+  else hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 8>), grid, block, 0, s, x, ldx, q, ldq, scales, n);
+}
+
+template <int DT>
+static hipError_t launch_quantize_t(int rows, int n, const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scales,
+                                    hipStream_t s) {
+  constexpr int VEC = DT == kF32 ? 4 : 8;
+  const bool aligned = (uintptr_t)x % 16 == 0 && (uintptr_t)q % VEC == 0 &&
+                       (rows == 1 || (ldx % VEC == 0 && ldq % VEC == 0));
+  const int pieces = n / VEC;
+  if (aligned && pieces <= 256 && pieces >= 1) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
+  else if (aligned && pieces <= 8 * 256 && rows > 512) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
+  else if (aligned && pieces <= 8 * 1024 && pieces >= 1) launch_quantize_rows<DT, 1024>(rows, n, x, ldx, q, ldq, scales, s);
+  else if (n <= 1024) hipLaunchKernelGGL((quantize_any_kernel<DT, 256>), dim3((unsigned)rows), dim3(256), 0, s, x, ldx, q, ldq, scales, n);
+  else hipLaunchKernelGGL((quantize_any_kernel<DT, 1024>), dim3((unsigned)rows), dim3(1024), 0, s, x, ldx, q, ldq, scales, n);
+  return hipGetLastError();
 }
 
 hipError_t launch_int8_quantize(int rows, int n, const void* x, int dtype, int64_t ldx, int8_t* q, int64_t ldq,
                                 float* scales, hipStream_t s) {
-  const dim3 grid((unsigned)rows), block(256);
-  if (dtype == kF32) hipLaunchKernelGGL(quantize_kernel<kF32>, grid, block, 0, s, x, ldx, q, ldq, scales, n);
-  else if (dtype == kF16) hipLaunchKernelGGL(quantize_kernel<kF16>, grid, block, 0, s, x, ldx, q, ldq, scales, n);
-  else hipLaunchKernelGGL(quantize_kernel<kBf16>, grid, block, 0, s, x, ldx, q, ldq, scales, n);
-  return hipGetLastError();
+  if (dtype == kF32) return launch_quantize_t<kF32>(rows, n, x, ldx, q, ldq, scales, s);
+  if (dtype == kF16) return launch_quantize_t<kF16>(rows, n, x, ldx, q, ldq, scales, s);
+  return launch_quantize_t<kBf16>(rows, n, x, ldx, q, ldq, scales, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -150,12 +267,34 @@ static hipError_t launch_rows(const Int8Args& a, int tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_int8_gemm(const Int8Args& a, hipStream_t s) {
-  const int avg = a.offsets ? (a.M + a.experts - 1) / a.experts : a.M;
-  if (avg <= 16) return launch_rows<1, 1>(a, row_tiles(a, 16), s);
-  if (avg <= 32) return launch_rows<2, 2>(a, row_tiles(a, 32), s);
-  if (avg > 128) return launch_int8_tile(a, s);
-  return launch_rows<4, 2>(a, row_tiles(a, 64), s);
+// Outputs and rows of the tile shapes of int8_tile.hip.
+struct TileSize {
+  int out, rows;
+};
+constexpr TileSize kTiles[] = {{256, 256}, {128, 128}, {128, 64}, {128, 32}, {256, 256}, {256, 128}, {128, 128}, {256, 128}, {128, 128}, {256, 128}, {128, 256}, {64, 64}, {256,128},{128,128},{128,128},{128,128},{256,128},{256,128},{128,64},{128,32},{64,64},{64,32},{128,32}};
+
+Int8Plan int8_plan(int M, int m, int n, int experts) {
+  const int avg = experts > 0 ? (M + experts - 1) / experts : M;
+  if (avg <= 16) return {-1, 1};
+  if (avg <= 32) return {3, 1};
+  if (avg <= 64) return {2, 1};
+  if (avg <= 128) return {1, 1};
+  return {0, 1};
+}
+
+size_t int8_partial_bytes(int M, int m, int n) {
+  const Int8Plan p = int8_plan(M, m, n, 0);
+  if (p.splits <= 1) return 0;
+  const TileSize t = kTiles[p.shape];
+  return (size_t)((m + t.out - 1) / t.out) * ((M + t.rows - 1) / t.rows) * p.splits * t.out * t.rows * 4;
+}
+
+hipError_t launch_int8_gemm(const Int8Args& args, hipStream_t s) {
+  Int8Args a = args;
+  const Int8Plan p = int8_plan(a.M, a.m, a.n, a.offsets ? a.experts : 0);
+  a.splits = p.splits;
+  if (p.shape >= 0) return launch_int8_tile(a, p.shape, s);
+  return launch_rows<1, 1>(a, row_tiles(a, 16), s);
 }
 
 }  // namespace tg

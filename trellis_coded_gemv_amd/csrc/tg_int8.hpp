@@ -99,6 +99,6 @@ inline int row_tiles(const Int8Args& a, int rows_per_tile) {
   return a.M / rows_per_tile + (a.experts < a.M ? a.experts : a.M);
 }
 
-hipError_t launch_int8_tile(const Int8Args& a, hipStream_t s);
+hipError_t launch_int8_tile(const Int8Args& a, int shape, hipStream_t s);
 
 }  // namespace tg

@@ -159,7 +159,19 @@ struct Int8Args {
   int32_t experts, pairs_per_row;
   int32_t out;            // kF32, kF16, kBf16
   int32_t wide_y;         // four neighbouring outputs of a row can be stored at once
+  int32_t splits;         // parts of the inner axis (dense only)
+  uint32_t* counters;     // a tile's arrivals, zero between calls
+  uint64_t* partials;     // [tiles][splits] sums of a workgroup's lanes
 };
+// The kernel and the split of the inner axis that a product takes.
+struct Int8Plan {
+  int shape;              // -1: rows straight to registers; else a tile shape of int8_tile.hip
+  int splits;
+};
+Int8Plan int8_plan(int M, int m, int n, int experts);   // experts 0: a dense product
+constexpr int kInt8Counters = 1024;
+constexpr size_t kInt8Partials = kWsHeader + 4 * kInt8Counters;   // offset in the workspace
+size_t int8_partial_bytes(int M, int m, int n);
 hipError_t launch_int8_quantize(int rows, int n, const void* x, int dtype, int64_t ldx, int8_t* q, int64_t ldq,
                                 float* scales, hipStream_t s);
 hipError_t launch_int8_gemm(const Int8Args& a, hipStream_t s);

@@ -436,7 +436,7 @@ def _common_device(where: str, *tensors) -> int:
 
 def _elsewhere(torch, at: int, stream) -> bool:
     """Whether a call has to enter another device or stream than the current ones."""
-    return stream is not None or at != torch.cuda.current_device()
+    return stream is not None or at != torch._C._cuda_getDevice()
 
 
 class _Entered:

@@ -7,9 +7,13 @@ namespace tg {
 
 namespace {
 
-// 16 bytes of global memory per lane to LDS at base + 16 * lane (base wave-uniform).
+// 16 bytes of global memory per lane to LDS at base + 16 * lane (base wave-uniform): from a lane's own address, or from
+// a lane's offset to a wave-uniform address.
 __device__ __forceinline__ void load_to_lds(const int8_t* p, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_base), "v"(p) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_base), "v"(p) : "memory");
+}
+__device__ __forceinline__ void load_to_lds(const int8_t* p, uint32_t offset, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(offset), "s"(p) : "memory");
 }
 
 // Wait until at most N of this wave's loads are in flight and its LDS reads are done.
@@ -79,7 +83,10 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
     ot = in / high;
     rt = band * 8 + in - ot * high;
   }
-  const RowTile tile = find_tile(a, rt, TX);
+  RowTile tile = find_tile(a, rt, TX);
+  tile.expert = __builtin_amdgcn_readfirstlane(tile.expert);
+  tile.first = __builtin_amdgcn_readfirstlane(tile.first);
+  tile.count = __builtin_amdgcn_readfirstlane(tile.count);
   if (tile.count <= 0) return;
   const int o0 = ot * TO;
   const int wo = wave % S::WO, wx = wave / S::WO;
@@ -89,13 +96,15 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
   // 16 AT wo + 4 AT g + 4 t + v, so that a lane ends with 4 AT neighbouring outputs of a row.
   const int lrow = lane / (BK / 16);
   auto piece = [&](int i) { return 16 * ((lane % (BK / 16)) ^ S::swizzle(S::RPI * i + lrow)); };   // of instruction i
-  const int8_t* wp[S::LW];
+  // The layer's rows are addressed by 32-bit offsets to the tile's first row (the launch keeps their stride below 2^23).
+  const int8_t* wbase = a.w + ((int64_t)tile.expert * a.m + o0) * a.ldw;
+  uint32_t woff[S::LW];
   const int8_t* xp[S::LX];
 #pragma unroll
   for (int i = 0; i < S::LW; ++i) {
     const int q = S::RPI * (S::LW * wave + i) + lrow;
-    const int o = o0 + q / (16 * AT) * (16 * AT) + 4 * AT * ((q >> 2) & 3) + 4 * ((q >> 4) % AT) + (q & 3);
-    wp[i] = a.w + ((int64_t)tile.expert * a.m + min(o, a.m - 1)) * a.ldw;
+    const int o = q / (16 * AT) * (16 * AT) + 4 * AT * ((q >> 2) & 3) + 4 * ((q >> 4) % AT) + (q & 3);
+    woff[i] = (uint32_t)min(o, a.m - 1 - o0) * (uint32_t)a.ldw;
   }
 #pragma unroll
   for (int i = 0; i < S::LX; ++i) {
@@ -106,11 +115,11 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
   const uint32_t wfill = __builtin_amdgcn_readfirstlane(sh0 + wave * S::LW * 1024);
   const uint32_t xfill = __builtin_amdgcn_readfirstlane(sh0 + TO * BK + wave * S::LX * 1024);
   auto load = [&](int step, uint32_t buf) {
-    // pieces past the end: any bytes of the row, not multiplied
+    const int k = step * BK, most = a.n - 16 - k;    // pieces past the end: any bytes of the row, not multiplied
 #pragma unroll
-    for (int i = 0; i < S::LW; ++i) load_to_lds(wp[i] + min(step * BK + piece(i), a.n - 16), wfill + buf + i * 1024);
+    for (int i = 0; i < S::LW; ++i) load_to_lds(wbase, woff[i] + (uint32_t)(k + min(piece(i), most)), wfill + buf + i * 1024);
 #pragma unroll
-    for (int i = 0; i < S::LX; ++i) load_to_lds(xp[i] + min(step * BK + piece(i), a.n - 16), xfill + buf + i * 1024);
+    for (int i = 0; i < S::LX; ++i) load_to_lds(xp[i] + (k + min(piece(i), most)), xfill + buf + i * 1024);
   };
 
   i32x4 acc[AT][RX];
@@ -120,46 +129,71 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
     for (int r = 0; r < RX; ++r) acc[t][r] = i32x4{0, 0, 0, 0};
   const int slot = 16 * (g ^ S::swizzle(j));     // of the step's first 64 bytes; the h-th 64: slot ^ 64 h
   const int abase = (wo * 16 * AT + j) * BK + slot, bbase = TO * BK + (wx * 16 * RX + j) * BK + slot;
-  auto multiply = [&](uint32_t buf, int left, auto last) {
+  // The operands of 64 bytes of the inner axis: read from LDS while the matrix cores work on those before.
+  struct Frags {
+    i32x4 a[AT], b[RX];
+  };
+  auto read = [&](Frags& f, uint32_t buf, int h) {
     const int8_t* at = sh + buf;
 #pragma unroll
-    for (int h = 0; h < BK / 64; ++h) {
-      i32x4 av[AT], bv[RX];
+    for (int r = 0; r < RX; ++r) f.b[r] = *reinterpret_cast<const i32x4*>(at + ((bbase ^ (64 * h)) + r * 16 * BK));
 #pragma unroll
-      for (int r = 0; r < RX; ++r) bv[r] = *reinterpret_cast<const i32x4*>(at + ((bbase ^ (64 * h)) + r * 16 * BK));
+    for (int t = 0; t < AT; ++t) f.a[t] = *reinterpret_cast<const i32x4*>(at + ((abase ^ (64 * h)) + t * 16 * BK));
+  };
+  auto cut = [&](Frags& f, int h, int left) {    // pieces past the end of the inner axis count as zero
+    if (64 * h + 16 * g >= left) {
 #pragma unroll
-      for (int t = 0; t < AT; ++t) av[t] = *reinterpret_cast<const i32x4*>(at + ((abase ^ (64 * h)) + t * 16 * BK));
-      if (decltype(last)::value && 64 * h + 16 * g >= left) {
-#pragma unroll
-        for (int r = 0; r < RX; ++r) bv[r] = i32x4{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int t = 0; t < AT; ++t)
-#pragma unroll
-        for (int r = 0; r < RX; ++r) acc[t][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[t], bv[r], acc[t][r], 0, 0, 0);
+      for (int r = 0; r < RX; ++r) f.b[r] = i32x4{0, 0, 0, 0};
     }
+  };
+  auto multiply = [&](const Frags& f) {
+#pragma unroll
+    for (int t = 0; t < AT; ++t)
+#pragma unroll
+      for (int r = 0; r < RX; ++r) acc[t][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[t], f.b[r], acc[t][r], 0, 0, 0);
   };
   const int steps_all = (a.n + BK - 1) / BK;
   const int begin = (int)((int64_t)steps_all * sp / a.splits), end = (int)((int64_t)steps_all * (sp + 1) / a.splits);
+  constexpr int U = BK / 64, LPS = S::LW + S::LX;
   uint32_t buf = 0;                               // of step s
   auto next = [](uint32_t b) { return b == (uint32_t)(ST - 1) * S::BUF ? 0u : b + S::BUF; };
 #pragma unroll
-  for (int i = 0; i < ST - 1; ++i) load(begin + i, i * S::BUF);
+  for (int i = 0; i < ST; ++i) load(min(begin + i, end - 1), i * S::BUF);
+  wait_loads<(ST - 1) * LPS>();
+  __builtin_amdgcn_s_barrier();
+  Frags f[2];
+  read(f[0], 0, 0);
   int s = begin;
-  for (; s < end - (ST - 1); ++s) {
-    wait_loads<(ST - 2) * (S::LW + S::LX)>();     // step s is in LDS, and this wave is done with step s - 1's buffer
-    __builtin_amdgcn_s_barrier();
-    load(s + ST - 1, buf == 0 ? (ST - 1) * S::BUF : buf - S::BUF);
-    multiply(buf, BK, std::false_type{});
-    buf = next(buf);
+  // A step: its 64-byte parts in turn, the next part read ahead. Before the next step's first part is read, its loads
+  // have landed and every wave holds this step's last part, so this step's buffer is free for the loads of step s + ST.
+  auto step = [&](auto more) {
+#pragma unroll
+    for (int h = 0; h < U; ++h) {
+      if (h == U - 1) {
+        wait_loads<decltype(more)::value ? (ST - 2) * LPS : 0>();
+        __builtin_amdgcn_s_barrier();
+        if constexpr (decltype(more)::value) load(s + ST, buf);
+        buf = next(buf);
+        read(f[(h + 1) & 1], buf, 0);
+      } else {
+        read(f[(h + 1) & 1], buf, h + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(f[h & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (U == 1) f[0] = f[1];
+  };
+  for (; s < end - ST; ++s) step(std::true_type{});
+  for (; s < end - 1; ++s) step(std::false_type{});
+  const int left = a.n - s * BK;
+#pragma unroll
+  for (int h = 0; h < U; ++h) {
+    if (h < U - 1) read(f[(h + 1) & 1], buf, h + 1);
+    cut(f[h & 1], h, left);
+    multiply(f[h & 1]);
   }
   wait_loads<0>();
-  __builtin_amdgcn_s_barrier();
-  for (; s < end - 1; ++s) {
-    multiply(buf, BK, std::false_type{});
-    buf = next(buf);
-  }
-  multiply(buf, a.n - s * BK, std::true_type{});
 
   // Split inner axis: every workgroup of the tile leaves its sums, the last to arrive adds the others' (whole
   // numbers: the order does not matter) and goes on.

@@ -519,9 +519,9 @@ int32_t int8_quantize(int32_t rows, int32_t n, const void *x, int32_t dtype, int
  * The sums are exact (int32); an output is rounded in binary32 as it is written here, and once more to a
  * 16-bit out_dtype.
  *   M  : 1 .. 2^20 rows; m : 1 .. 2^22 outputs; n : a multiple of 16 up to 131056 (so that no sum leaves
- *        int32, 128 * 128 * n < 2^31).
+ *        int32, 128 * 128 * n < 2^31); M * m <= 2^38.
  *   xq : device, M rows of n int8, 16-byte aligned, row stride ldx >= n bytes, a multiple of 16.
- *   xs : device, M fp32. wq : device, m rows of n int8, aligned as xq. wscales : device, m fp32.
+ *   xs : device, M fp32. wq : device, m rows of n int8, aligned as xq, ldw <= 2^23. wscales : device, m fp32.
  *   Y  : device, M rows of m values of type out_dtype, row stride ldy >= m elements.
  *   ws : device workspace, ws_bytes >= tg_int8_workspace_size(M, m, n), 256-byte aligned, zero-filled
  *        before its first use; every call leaves its counters at zero, so one buffer, as large as each

@@ -138,6 +138,80 @@ def test_gemm_matches_oracle(M, m, n, px, pw, py, dtype):
         assert bool((wide[0] == 9).all()) and bool((wide[-1] == 9).all()) and bool((wide[:, m:] == 9).all())
 
 
+LARGE = [  # one or more products for each tile shape and for split inner axes; odd sizes, ends inside a step
+    (3001, 4001, 4112), (1500, 5003, 2064), (301, 20001, 1040), (1030, 9000, 272), (100, 30001, 1040), (515, 4099, 2064), (260, 4100, 4112),
+    (150, 28674, 144), (61, 4096, 14336), (64, 4097, 14352), (1, 28672, 8192), (1, 28673, 176), (256, 4096, 14336), (2050, 300, 20000)]
+
+
+def _device_ref(torch, xq, xs, wq, ws):
+    """The exact sums by binary64 products on the device (below 2^53), and their scaled values in binary64."""
+    return (xq.double() @ wq.double().t()) * xs.double()[:, None] * ws.double()
+
+
+def _near_on_device(torch, y, ref, dtype):
+    bound = TOL[dtype] * ref.abs() + (2.0 ** -25 if dtype == "float16" else 2.0 ** -149)
+    assert bool((y.double() - ref).abs().le(bound).all())
+
+
+@pytest.mark.parametrize("M,m,n", LARGE)
+def test_gemm_large_tiles(M, m, n):
+    dev = device()
+    import torch
+    say("int8 gemm large", M, m, n)
+    g = torch.Generator(device=dev).manual_seed(M + m + n)
+    q = lambda *s: torch.randint(-128, 128, s, generator=g, device=dev, dtype=torch.int8)
+    xq, wq = q(M, n + 16)[:, :n], q(m, n)
+    xs, ws = torch.rand(M, generator=g, device=dev) * 0.01 + 0.001, torch.rand(m, generator=g, device=dev) * 0.01 + 0.001
+    L = tg.Int8Layer(wq, ws)
+    work = tg.int8_workspace(L, M)
+    ref = _device_ref(torch, xq, xs, wq, ws)
+    first = None
+    for dtype in ("float32", "bfloat16", "float16", "float32"):
+        Y = torch.full((M + 1, m + 3), 9.0, dtype=getattr(torch, dtype), device=dev)
+        tg.int8_gemm(L, xq, xs, Y=Y[:M, :m], ws=work)
+        torch.cuda.synchronize()
+        _near_on_device(torch, Y[:M, :m], ref, dtype)
+        assert bool((Y[M] == 9).all()) and bool((Y[:, m:] == 9).all())
+        if dtype == "float32":
+            assert first is None or torch.equal(first, Y)            # the same bits, however the parts arrive
+            first = Y
+    assert not bool(work[256:256 + 4096].any())                      # counters back at zero
+
+
+LARGE_GROUPED = [(4000, 4100, 4112, 2, 2), (1000, 2100, 272, 3, 3), (3000, 5000, 2064, 2, 1), (300, 1540, 2064, 16, 2), (2048, 1536, 2048, 128, 8),
+                 (60, 9000, 1040, 3, 4), (1000, 600, 144, 12, 8), (8192, 260, 768, 200, 8), (30, 33, 528, 1000, 6)]
+
+
+@pytest.mark.parametrize("tokens,m,n,experts,top_k", LARGE_GROUPED)
+@pytest.mark.parametrize("shared", [True, False])
+def test_grouped_large_tiles(tokens, m, n, experts, top_k, shared):
+    """Each tile shape over ragged groups: an even routing with one crowded expert, some without pairs, some ids that are no expert."""
+    dev = device()
+    import torch
+    say("int8 grouped large", tokens, m, n, experts, top_k, shared)
+    g = torch.Generator(device=dev).manual_seed(tokens + m + n)
+    q = lambda *s: torch.randint(-128, 128, s, generator=g, device=dev, dtype=torch.int8)
+    pairs, ppr = tokens * top_k, top_k if shared else 1
+    sel = torch.randint(-1, experts, (pairs,), generator=g, device=dev, dtype=torch.int32)
+    if experts > 3:
+        sel[torch.rand(pairs, generator=g, device=dev) < 0.2] = 1
+        sel[sel == 2] = 3
+    off, order = tg.moe_group(sel, experts)
+    xq, wq = q(pairs // ppr, n), q(experts, m, n)
+    xs = torch.rand(pairs // ppr, generator=g, device=dev) * 0.01 + 0.001
+    ws = torch.rand(experts, m, generator=g, device=dev) * 0.01 + 0.001
+    Y = torch.full((pairs, m), 9.0, device=dev)
+    tg.int8_gemm_grouped(tg.Int8Experts(wq, ws), xq, xs, off, order, ppr, Y=Y)
+    torch.cuda.synchronize()
+    rows = torch.arange(pairs, device=dev) // ppr
+    for e in range(-1, experts):
+        p = (sel == e).nonzero()[:, 0]
+        if e < 0:
+            assert bool((Y[p] == 9).all())
+        elif len(p):
+            _near_on_device(torch, Y[p], _device_ref(torch, xq[rows[p]], xs[rows[p]], wq[e], ws[e]), "float32")
+
+
 @pytest.mark.parametrize("M", [1, 40, 300])
 def test_gemm_largest_sums(M):
     """-128 * -128 over the longest axis: 2^31 - 2^18, still inside int32."""

@@ -70,7 +70,7 @@ SHARED = [(dict(m=0), -2), (dict(m=(1 << 22) + 1, ldy=1 << 23), -2), (dict(n=0),
 
 
 @pytest.mark.parametrize("kw,status", SHARED + [
-    (dict(M=0), -2), (dict(M=(1 << 20) + 1), -2), (dict(ldw=112), -8), (dict(ldw=136), -8), (dict(ws=0), -5),
+    (dict(M=0), -2), (dict(M=(1 << 20) + 1), -2), (dict(ldw=112), -8), (dict(ldw=136), -8), (dict(ldw=(1 << 23) + 16), -8), (dict(ws=0), -5),
     (dict(ws_bytes=255), -5), (dict(ws=A16 + 16), -4)])
 def test_gemm_refusals(kw, status):
     assert _gemm(**kw) == status
@@ -85,10 +85,10 @@ def test_grouped_refusals(kw, status):
 
 def test_workspace_sizes():
     L = tg.lib()
-    for M, m, n in ((1, 1, 16), (64, 4096, 14336), (4096, 28672, 8192), (1 << 20, 1 << 22, 131056)):
+    for M, m, n in ((1, 1, 16), (64, 4096, 14336), (4096, 28672, 8192), (1 << 20, 1 << 18, 131056), (1 << 16, 1 << 22, 16)):
         size = L.tg_int8_workspace_size(M, m, n)
         assert size >= 256 and size % 256 == 0
-    for M, m, n in ((0, 1, 16), (1, 0, 16), (1, 1, 8), (1, 1, 131072), ((1 << 20) + 1, 1, 16)):
+    for M, m, n in ((0, 1, 16), (1, 0, 16), (1, 1, 8), (1, 1, 131072), ((1 << 20) + 1, 1, 16), (1 << 20, 1 << 22, 16)):
         assert L.tg_int8_workspace_size(M, m, n) == 0
 
 

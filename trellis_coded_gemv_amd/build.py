@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtrellis_gemv.so")
 SOURCES = ["api.hip", "gemv.hip", "fused.hip", "gemm_small.hip", "misc.hip", "encode.hip", "prefill.hip",
-           "route.hip", "int8.hip", "int8_tile.hip"]
+           "route.hip", "int8_quantize.hip", "int8_gemm.hip"]
 ROCM_LIB = "/opt/rocm/lib"
 ARCH = "gfx950"
 

@@ -741,17 +741,20 @@ size_t type_size(int32_t dtype) { return dtype == TG_F32 ? 4 : 2; }
 
 // 128 * 128 * n < 2^31: no sum of 8-bit products leaves int32.
 constexpr int32_t kInt8MaxN = 131056;
+// A tile's 256 layer rows are addressed by 32-bit offsets to the first.
+constexpr int64_t kInt8MaxStride = 1 << 23;
 
 int32_t check_int8_shape(int32_t rows, int32_t m, int32_t n) {
   if (rows < 1 || rows > (1 << 20) || m < 1 || m > (1 << 22) || n < 16 || n % 16 != 0 || n > kInt8MaxN)
     return TG_ERR_SHAPE;
-  return TG_OK;
+  return (int64_t)rows * m <= kMaxDenseWeights ? TG_OK : TG_ERR_SHAPE;
 }
 
 // The operands that a dense product and the experts' share, after the shape has been checked.
 int32_t check_int8_operands(const Int8Args& a) {
   if (!a.x || !a.xs || !a.w || !a.ws || !a.y) return TG_ERR_NULL;
-  if (bad_type(a.out) || a.ldx < a.n || a.ldx % 16 != 0 || a.ldw < a.n || a.ldw % 16 != 0 || a.ldy < a.m)
+  if (bad_type(a.out) || a.ldx < a.n || a.ldx % 16 != 0 || a.ldw < a.n || a.ldw % 16 != 0 || a.ldw > kInt8MaxStride ||
+      a.ldy < a.m)
     return TG_ERR_ARG;
   if (misaligned(a.x, 16) || misaligned(a.w, 16) || misaligned(a.xs, 4) || misaligned(a.ws, 4) ||
       misaligned(a.y, type_size(a.out)))

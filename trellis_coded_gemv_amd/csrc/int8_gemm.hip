@@ -1,0 +1,518 @@
+// Products of 8-bit rows: Y[r, o] = (sum_i xq[r, i] wq[o, i]) * xs[r] * ws[o], for a dense layer and for the experts of
+// routed pairs, by tiles of TO outputs x TX rows.
+//
+// The sums are exact in int32 (|q| <= 128 and n < 2^17, so none leaves the type), whatever the order and the split of the
+// work; an output is rounded three times in binary32 (the sum, and its product with either scale) and once more to a
+// 16-bit output type.
+//
+// v_mfma_i32_16x16x64_i8 with the layer's rows as its A operand and the activation rows as its B operand: lane l
+// supplies row l % 16 and the 16 bytes at 16 (l / 16) of 64 bytes of the inner axis on both sides, and ends with four
+// neighbouring outputs of row l % 16. Both sides reach LDS by loads that do not pass through registers, a ring of ST
+// steps of BK bytes, and the operands are read from there.
+#include <type_traits>
+
+#include "tg_device.hpp"
+#include "tg_internal.hpp"
+
+namespace tg {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast 15 to rows 1 and 3, 31 to rows 2 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
+// A workgroup's tile. rows: dense, output rows first .. first + count - 1; experts, places first .. of order.
+struct Tile {
+  int ot, rt, sp;             // output tile, row tile, part of the inner axis
+  int expert, first, count;   // count 0: nothing to do
+};
+
+// Workgroup -> tile. Workgroups b, b + 8, ... share an XCD and its L2: each XCD takes a run of neighbouring tiles out of
+// those that there are, the same number for each. Dense: 8 row tiles by all output tiles, rows first, so that an XCD's
+// resident workgroups share a few row tiles and output tiles. Experts: the row tiles are numbered expert by expert (every
+// wave finds them from the offsets, up to 16 neighbouring experts to a lane), outputs first, so that an expert's tiles
+// stay together; the launch holds the most tiles that the pairs could need, and what is over ends at once.
+// Every value is wave-uniform.
+__device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int row_tiles, int rows_per_tile) {
+  constexpr int kHeld = 4;                      // experts of a lane whose places are kept
+  Tile t{0, 0, 0, 0, 0, 0};
+  const int lane = threadIdx.x & 63;
+  const int per_lane = (a.experts + 63) >> 6;
+  int b[kHeld], c[kHeld], mine = 0, scan = 0;
+  auto place = [&](int e, int& from, int& to) {
+    from = to = 0;
+    if (e < a.experts) {
+      from = min(max(a.offsets[e], 0), a.M);
+      to = max(min(max(a.offsets[e + 1], 0), a.M), from);
+    }
+  };
+  auto tiles = [&](int from, int to) { return (to - from + rows_per_tile - 1) / rows_per_tile; };
+  if (a.offsets) {
+    if (per_lane <= kHeld) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        place(i < per_lane ? lane * per_lane + i : a.experts, b[i], c[i]);
+        mine += tiles(b[i], c[i]);
+      }
+    } else {
+      for (int i = 0; i < per_lane; ++i) {
+        int from, to;
+        place(lane * per_lane + i, from, to);
+        mine += tiles(from, to);
+      }
+    }
+    scan = wave_scan(mine);
+    row_tiles = min(row_tiles, __builtin_amdgcn_readlane(scan, 63));
+  }
+  int id;
+  {
+    const int all = out_tiles * row_tiles * a.splits;
+    const int per = all >> 3, rest = all & 7, x = blockIdx.x & 7, k = blockIdx.x >> 3;
+    if (k >= per + (x < rest ? 1 : 0)) return t;
+    id = x * per + min(x, rest) + k;
+  }
+  if (a.splits > 1) {
+    const int q = id / a.splits;
+    t.sp = id - q * a.splits;
+    id = q;
+  }
+  if (!a.offsets) {
+    const int band = id / (8 * out_tiles), in = id - band * 8 * out_tiles;
+    const int high = min(8, row_tiles - band * 8);
+    t.ot = in / high;
+    t.rt = band * 8 + in - t.ot * high;
+    t.first = t.rt * rows_per_tile;
+    t.count = min(rows_per_tile, a.M - t.first);
+    return t;
+  }
+  t.rt = id / out_tiles;
+  t.ot = id - t.rt * out_tiles;
+  const int owner = __builtin_ctzll(__ballot(scan > t.rt));     // some lane is, as rt < the last lane's sum
+  int left = t.rt - __builtin_amdgcn_readlane(scan - mine, owner);
+  for (int i = 0; i < per_lane; ++i) {
+    int from, to;
+    if (per_lane <= kHeld) {
+      int bi = b[0], ci = c[0];
+#pragma unroll
+      for (int h = 1; h < kHeld; ++h) {
+        bi = i == h ? b[h] : bi;
+        ci = i == h ? c[h] : ci;
+      }
+      from = __builtin_amdgcn_readlane(bi, owner);
+      to = __builtin_amdgcn_readlane(ci, owner);
+    } else {
+      place(owner * per_lane + i, from, to);
+      from = __builtin_amdgcn_readfirstlane(from);
+      to = __builtin_amdgcn_readfirstlane(to);
+    }
+    const int n = tiles(from, to);
+    if (left < n) {
+      t.expert = owner * per_lane + i;
+      t.first = from + left * rows_per_tile;
+      t.count = min(rows_per_tile, to - t.first);
+      return t;
+    }
+    left -= n;
+  }
+  return t;
+}
+
+// Output row (pair) of row i of a tile, or -1; its activation row is pair / pairs_per_row.
+__device__ __forceinline__ int pair_of(const Int8Args& a, const Tile& t, int i) {
+  if (i >= t.count) return -1;
+  if (!a.offsets) return t.first + i;
+  const int p = a.order[t.first + i];
+  return p >= 0 && p < a.M ? p : -1;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t half_bits(float v) {
+  if constexpr (DT == kF16) return __builtin_bit_cast(uint16_t, (_Float16)v);
+  return __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+
+// Four neighbouring outputs of a row, of which `valid` exist. wide: they may be stored at once.
+template <int DT>
+__device__ __forceinline__ void store4(void* y, int64_t at, const float (&v)[4], int valid, bool wide) {
+  if constexpr (DT == kF32) {
+    float* p = reinterpret_cast<float*>(y) + at;
+    if (valid >= 4 && wide) *reinterpret_cast<float4_t*>(p) = float4_t{v[0], v[1], v[2], v[3]};
+    else
+      for (int i = 0; i < 4; ++i)
+        if (i < valid) p[i] = v[i];
+  } else {
+    uint16_t* p = reinterpret_cast<uint16_t*>(y) + at;
+    if (valid >= 4 && wide)
+      *reinterpret_cast<u32x2*>(p) = u32x2{half_bits<DT>(v[0]) | half_bits<DT>(v[1]) << 16,
+                                           half_bits<DT>(v[2]) | half_bits<DT>(v[3]) << 16};
+    else
+      for (int i = 0; i < 4; ++i)
+        if (i < valid) p[i] = (uint16_t)half_bits<DT>(v[i]);
+  }
+}
+
+namespace {
+
+// Row tiles of a launch: exact for a dense product; for the experts' an upper bound that holds for every way the
+// pairs can fall (each expert with pairs leaves at most one tile part-filled).
+int row_tiles(const Int8Args& a, int rows_per_tile) {
+  const int full = (a.M + rows_per_tile - 1) / rows_per_tile;
+  if (!a.offsets) return full;
+  return a.M / rows_per_tile + (a.experts < a.M ? a.experts : a.M);
+}
+
+// 16 bytes of global memory per lane to LDS at base + 16 * lane (base wave-uniform): from a lane's own address, or from
+// a lane's offset to a wave-uniform address.
+__device__ __forceinline__ void load_to_lds(const int8_t* p, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_base), "v"(p) : "memory");
+}
+__device__ __forceinline__ void load_to_lds(const int8_t* p, uint32_t offset, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(offset), "s"(p) : "memory");
+}
+
+// Wait until at most N of this wave's loads are in flight and its LDS reads are done.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void put_partial(uint64_t* p, i32x4 v) {
+  const u32x4 u = __builtin_bit_cast(u32x4, v);
+  __hip_atomic_store(p, (uint64_t)u[1] << 32 | u[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(p + 1, (uint64_t)u[3] << 32 | u[2], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ i32x4 get_partial(uint64_t* p) {
+  const uint64_t a = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint64_t b = __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return i32x4{(int)(uint32_t)a, (int)(a >> 32), (int)(uint32_t)b, (int)(b >> 32)};
+}
+
+// AT x RX: 16x16 tiles of one wave (outputs x rows); WO x WX: waves of a workgroup; BK: bytes of the inner axis per
+// step; ST: steps held in LDS, of the layer's side EW more.
+template <int AT_, int RX_, int WO_, int WX_, int BK_, int ST_, int EW_ = 0, int OCC_ = 2>
+struct TileShape {
+  static constexpr int AT = AT_, RX = RX_, WO = WO_, WX = WX_, BK = BK_, ST = ST_, EW = EW_, OCC = OCC_;
+  static constexpr bool AHEAD = OCC <= 2;                            // registers for two sets of operands
+  static constexpr int NW = WO * WX, TO = 16 * AT * WO, TX = 16 * RX * WX;
+  static constexpr int RPI = 1024 / BK;                             // LDS rows filled by one load instruction
+  static constexpr int LW = TO / RPI / NW, LX = TX / RPI / NW;      // load instructions of a wave per step
+  static constexpr int WBUF = TO * BK, XBUF = TX * BK;              // LDS bytes of a step
+  static constexpr int XLDS = (ST + EW) * WBUF;                     // where the activations' steps begin
+  static_assert(AHEAD || EW == 0, "");
+  static_assert(LW * RPI * NW == TO && LX * RPI * NW == TX, "every wave loads whole instructions");
+  // A row's 16-byte pieces are held in LDS in an order that depends on the row, so that the lanes which read the same
+  // piece of neighbouring rows spread over the banks.
+  static __device__ __forceinline__ int swizzle(int row) { return BK >= 128 ? row & 7 : (row >> 1) & 3; }
+};
+
+}  // namespace
+
+template <class S, int DT>
+__global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int8Args a, int out_tiles, int row_tiles) {
+  constexpr int AT = S::AT, RX = S::RX, BK = S::BK, ST = S::ST, TO = S::TO, TX = S::TX, NW = S::NW;
+  __shared__ __attribute__((aligned(1024))) int8_t sh[S::XLDS + ST * S::XBUF];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int j = lane & 15, g = lane >> 4;
+  const Tile tile = find_tile(a, out_tiles, row_tiles, TX);
+  if (tile.count <= 0) return;
+  const int ot = tile.ot, rt = tile.rt, sp = tile.sp;
+  const int o0 = ot * TO;
+  const int wo = wave % S::WO, wx = wave / S::WO;
+
+  // Loads: an instruction fills RPI rows of LDS; lane l the slot l % (BK / 16) of row l / (BK / 16), where the piece
+  // slot ^ swizzle(row) of the row belongs. LDS row 16 (AT wo + t) + 4 g + v of the layer's side holds output
+  // 16 AT wo + 4 AT g + 4 t + v, so that a lane ends with 4 AT neighbouring outputs of a row.
+  const int lrow = lane / (BK / 16);
+  auto wrow = [&](int i) { return S::RPI * (S::LW * wave + i) + lrow; };   // LDS row of this lane in instruction i
+  auto xrow = [&](int i) { return S::RPI * (S::LX * wave + i) + lrow; };
+  auto piece = [&](int row) { return 16 * ((lane % (BK / 16)) ^ S::swizzle(row)); };
+  // The layer's rows are addressed by 32-bit offsets to the tile's first row (the launch keeps their stride below 2^23).
+  const int8_t* wbase = a.w + ((int64_t)tile.expert * a.m + o0) * a.ldw;
+  uint32_t woff[S::LW];
+  const int8_t* xp[S::LX];
+#pragma unroll
+  for (int i = 0; i < S::LW; ++i) {
+    const int q = wrow(i);
+    const int o = q / (16 * AT) * (16 * AT) + 4 * AT * ((q >> 2) & 3) + 4 * ((q >> 4) % AT) + (q & 3);
+    woff[i] = (uint32_t)min(o, a.m - 1 - o0) * (uint32_t)a.ldw;
+  }
+#pragma unroll
+  for (int i = 0; i < S::LX; ++i) {
+    xp[i] = a.x + (int64_t)(max(pair_of(a, tile, xrow(i)), 0) / a.pairs_per_row) * a.ldx;
+  }
+  const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)sh;
+  const uint32_t wfill = __builtin_amdgcn_readfirstlane(sh0 + wave * S::LW * 1024);
+  const uint32_t xfill = __builtin_amdgcn_readfirstlane(sh0 + S::XLDS + wave * S::LX * 1024);
+  auto load_w = [&](int step, uint32_t buf) {
+    const int k = step * BK, most = a.n - 16 - k;    // pieces past the end: any bytes of the row, not multiplied
+#pragma unroll
+    for (int i = 0; i < S::LW; ++i) load_to_lds(wbase, woff[i] + (uint32_t)(k + min(piece(wrow(i)), most)), wfill + buf + i * 1024);
+  };
+  auto load_x = [&](int step, uint32_t buf) {
+    const int k = step * BK, most = a.n - 16 - k;
+#pragma unroll
+    for (int i = 0; i < S::LX; ++i) load_to_lds(xp[i] + (k + min(piece(xrow(i)), most)), xfill + buf + i * 1024);
+  };
+
+  i32x4 acc[AT][RX];
+#pragma unroll
+  for (int t = 0; t < AT; ++t)
+#pragma unroll
+    for (int r = 0; r < RX; ++r) acc[t][r] = i32x4{0, 0, 0, 0};
+  const int slot = 16 * (g ^ S::swizzle(j));     // of the step's first 64 bytes; the h-th 64: slot ^ 64 h
+  const int abase = (wo * 16 * AT + j) * BK + slot, bbase = S::XLDS + (wx * 16 * RX + j) * BK + slot;
+  // The operands of 64 bytes of the inner axis: read from LDS while the matrix cores work on those before.
+  struct Frags {
+    i32x4 a[AT], b[RX];
+  };
+  uint32_t wbuf = 0, xbuf = 0;                   // of step s
+  auto read = [&](Frags& f, int h) {
+#pragma unroll
+    for (int r = 0; r < RX; ++r) f.b[r] = *reinterpret_cast<const i32x4*>(sh + xbuf + ((bbase ^ (64 * h)) + r * 16 * BK));
+#pragma unroll
+    for (int t = 0; t < AT; ++t) f.a[t] = *reinterpret_cast<const i32x4*>(sh + wbuf + ((abase ^ (64 * h)) + t * 16 * BK));
+  };
+  auto cut = [&](Frags& f, int h, int left) {    // pieces past the end of the inner axis count as zero
+    if (64 * h + 16 * g >= left) {
+#pragma unroll
+      for (int r = 0; r < RX; ++r) f.b[r] = i32x4{0, 0, 0, 0};
+    }
+  };
+  auto multiply = [&](const Frags& f) {
+#pragma unroll
+    for (int t = 0; t < AT; ++t)
+#pragma unroll
+      for (int r = 0; r < RX; ++r) acc[t][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[t], f.b[r], acc[t][r], 0, 0, 0);
+  };
+  const int steps_all = (a.n + BK - 1) / BK;
+  const int begin = (int)((int64_t)steps_all * sp / a.splits), end = (int)((int64_t)steps_all * (sp + 1) / a.splits);
+  constexpr int U = BK / 64, EW = S::EW;
+  Frags f[2];
+  int s = begin;
+  auto advance = [&]() {
+    wbuf = wbuf == (uint32_t)(ST + EW - 1) * S::WBUF ? 0u : wbuf + S::WBUF;
+    xbuf = xbuf == (uint32_t)(ST - 1) * S::XBUF ? 0u : xbuf + S::XBUF;
+  };
+  if constexpr (S::AHEAD) {
+    // Loads in the order X(i), W(i + EW): what may still be in flight when X(i) and W(i) are needed.
+    constexpr int kAhead = (EW > 0 ? S::LW : 0) + (ST - 1) * (S::LW + S::LX);
+    if constexpr (EW > 0) load_w(begin, 0);
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+      load_x(min(begin + i, end - 1), i * S::XBUF);
+      load_w(min(begin + i + EW, end - 1), (i + EW) * S::WBUF);
+    }
+    wait_loads<kAhead>();
+    __builtin_amdgcn_s_barrier();
+    read(f[0], 0);
+    // A step: its 64-byte parts in turn, the next part read ahead. Before the next step's first part is read, its loads
+    // have landed and every wave holds this step's last part, so this step's buffers are free for loads.
+    auto step = [&](auto more) {
+#pragma unroll
+      for (int h = 0; h < U; ++h) {
+        if (h == U - 1) {
+          wait_loads<decltype(more)::value ? kAhead - (S::LW + S::LX) : 0>();
+          __builtin_amdgcn_s_barrier();
+          if constexpr (decltype(more)::value) {
+            load_x(s + ST, xbuf);
+            load_w(min(s + ST + EW, end - 1), wbuf);
+          }
+          advance();
+          read(f[(h + 1) & 1], 0);
+        } else {
+          read(f[(h + 1) & 1], h + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(f[h & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (U == 1) f[0] = f[1];
+    };
+    for (; s < end - ST; ++s) step(std::true_type{});
+    for (; s < end - 1; ++s) step(std::false_type{});
+    const int left = a.n - s * BK;
+#pragma unroll
+    for (int h = 0; h < U; ++h) {
+      if (h < U - 1) read(f[(h + 1) & 1], h + 1);
+      cut(f[h & 1], h, left);
+      multiply(f[h & 1]);
+    }
+  } else {
+    // Several workgroups share a compute unit: each reads and multiplies in turn, and they fill each other's waits.
+    constexpr int LPS = S::LW + S::LX;
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) {
+      load_x(min(begin + i, end - 1), i * S::XBUF);
+      load_w(min(begin + i, end - 1), i * S::WBUF);
+    }
+    for (; s < end - (ST - 1); ++s) {
+      wait_loads<(ST - 2) * LPS>();               // step s is in LDS, and this wave is done with step s - 1's buffers
+      __builtin_amdgcn_s_barrier();
+      load_x(s + ST - 1, xbuf == 0 ? (ST - 1) * S::XBUF : xbuf - S::XBUF);
+      load_w(s + ST - 1, wbuf == 0 ? (ST - 1) * S::WBUF : wbuf - S::WBUF);
+#pragma unroll
+      for (int h = 0; h < U; ++h) {
+        read(f[0], h);
+        multiply(f[0]);
+      }
+      advance();
+    }
+    wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    for (; s < end; ++s) {
+#pragma unroll
+      for (int h = 0; h < U; ++h) {
+        read(f[0], h);
+        if (s == end - 1) cut(f[0], h, a.n - s * BK);
+        multiply(f[0]);
+      }
+      advance();
+    }
+  }
+  wait_loads<0>();
+
+  // Split inner axis: every workgroup of the tile leaves its sums, the last to arrive adds the others' (whole
+  // numbers: the order does not matter) and goes on.
+  if (a.splits > 1) {
+    constexpr int T = 64 * NW;
+    uint64_t* mine = a.partials + ((size_t)(rt * out_tiles + ot) * a.splits + sp) * (2 * T * AT * RX) + 2 * threadIdx.x;
+#pragma unroll
+    for (int t = 0; t < AT; ++t)
+#pragma unroll
+      for (int r = 0; r < RX; ++r) put_partial(mine + 2 * T * (t * RX + r), acc[t][r]);
+    __syncthreads();                              // the operands' LDS is done with: its first word is the flag
+    if (!arrive_is_last(a.counters + rt * out_tiles + ot, a.splits, reinterpret_cast<uint32_t*>(sh))) return;
+    for (int o = 0; o < a.splits; ++o) {
+      if (o == sp) continue;
+      uint64_t* theirs = mine + ((ptrdiff_t)o - sp) * (2 * T * AT * RX);
+#pragma unroll
+      for (int t = 0; t < AT; ++t)
+#pragma unroll
+        for (int r = 0; r < RX; ++r) acc[t][r] += get_partial(theirs + 2 * T * (t * RX + r));
+    }
+    if (threadIdx.x == 0) reset_counter(a.counters + rt * out_tiles + ot);
+  }
+
+  // Lane: outputs o0 + 16 AT wo + 4 AT g + 4 t + v of row 16 RX wx + 16 r + j.
+  const int ob = o0 + 16 * AT * wo + 4 * AT * g;
+#pragma unroll
+  for (int r = 0; r < RX; ++r) {
+    const int p = pair_of(a, tile, 16 * (RX * wx + r) + j);
+    if (p < 0) continue;
+    const float xs = a.xs[p / a.pairs_per_row];
+#pragma unroll
+    for (int t = 0; t < AT; ++t) {
+      const int o = ob + 4 * t;
+      if (o >= a.m) continue;
+      float v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = (float)acc[t][r][c] * xs * a.ws[(int64_t)tile.expert * a.m + min(o + c, a.m - 1)];
+      store4<DT>(a.y, (int64_t)p * a.ldy + o, v, a.m - o, a.wide_y);
+    }
+  }
+}
+
+template <class S, int DT>
+static hipError_t launch_shape_t(const Int8Args& a, hipStream_t s) {
+  const int ot = (a.m + S::TO - 1) / S::TO, rt = row_tiles(a, S::TX);
+  const int64_t groups = (int64_t)ot * rt * a.splits;
+  if (groups * 64 * S::NW >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;   // more than a launch holds
+  hipLaunchKernelGGL((int8_tile_kernel<S, DT>), dim3((unsigned)groups), dim3(64 * S::NW), 0, s, a, ot, rt);
+  return hipGetLastError();
+}
+
+template <class S>
+static hipError_t launch_shape(const Int8Args& a, hipStream_t s) {
+  if (a.out == kF32) return launch_shape_t<S, kF32>(a, s);
+  if (a.out == kF16) return launch_shape_t<S, kF16>(a, s);
+  return launch_shape_t<S, kBf16>(a, s);
+}
+
+// The tile shapes. What one costs, measured over 13 layers (300 to 28672 outputs, 768 to 20000 inputs) at 1 to 8192 rows
+// and fitted: microseconds per 128 bytes of the inner axis for a compute unit that holds one workgroup, and for one that
+// holds two; microseconds per tile beside that (its first loads, its stores).
+struct TileCost {
+  int out, rows, resident;
+  float alone, shared, tile;
+};
+constexpr TileCost kTiles[] = {
+    {256, 256, 1, 1.80f, 1.80f, 5.6f},   // TileShape<4, 8, 4, 2, 128, 2, 1>
+    {256, 128, 1, 1.02f, 1.02f, 5.0f},   // TileShape<4, 4, 4, 2, 128, 3>
+    {256, 128, 2, 1.88f, 1.95f, 2.0f},   // TileShape<4, 4, 4, 2, 64, 3, 0, 4>: two workgroups fill each other's waits
+    {128, 128, 1, 0.60f, 0.60f, 2.0f},   // TileShape<2, 4, 4, 2, 128, 3>
+    {128, 64, 2, 0.35f, 0.79f, 1.4f},    // TileShape<2, 4, 4, 1, 128, 3>
+    {64, 32, 2, 0.13f, 0.25f, 1.15f},    // TileShape<1, 2, 4, 1, 256, 3>
+    {32, 16, 2, 0.057f, 0.14f, 0.64f},   // TileShape<1, 1, 2, 1, 512, 3>
+};
+constexpr float kStreamRate = 4.68e6f;   // bytes per microsecond of a product that waits for memory alone
+constexpr int kComputeUnits = 256;
+
+// The cheapest shape and split of the inner axis: rounds of workgroups over the compute units, and the time that the
+// bytes take, of which a part is not hidden behind the other. Against trying everything this loses 0.4% over the sweep,
+// where any one shape loses a factor of 1.3 to 20 somewhere. A split inner axis costs the parts' sums, so only products
+// with few tiles take one. Experts: row tiles as an even routing fills them, one half-filled for each expert.
+Int8Plan int8_plan(int M, int m, int n, int experts) {
+  const float reached = experts > 0 ? (float)(experts < M ? experts : M) : 1.f;
+  const float rows = (float)M / reached;
+  const float stream = (reached * m * (float)n + (float)M * n + 2.f * M * m) / kStreamRate;
+  const int steps = (n + 127) / 128;
+  Int8Plan best{0, 1};
+  float least = 3.0e38f;
+  for (int shape = 0; shape < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++shape) {
+    const TileCost& t = kTiles[shape];
+    if (t.rows > 32 && t.rows > 2.f * rows) continue;          // more than half of it empty
+    const float rt = experts > 0 ? reached * (rows / t.rows + 0.5f > 1.f ? rows / t.rows + 0.5f : 1.f)
+                                 : (float)((M + t.rows - 1) / t.rows);
+    const float tiles = rt * (float)((m + t.out - 1) / t.out);
+    const int slots = kComputeUnits * t.resident;
+    for (int splits : {1, 2, 3, 4, 6, 8}) {
+      if (splits > 1 && (experts > 0 || tiles > kInt8Counters / 2 || splits * 512 > n)) break;
+      const float groups = tiles * splits;
+      const float rounds = (float)(int64_t)(groups / slots), rest = groups - rounds * slots;
+      const float len = (float)((steps + splits - 1) / splits);
+      float work = rounds * (t.shared * len + t.tile);
+      if (rest > 0.f) work += (rest > kComputeUnits ? t.shared : t.alone) * len + t.tile;
+      float us = (work > stream ? work : stream) + 0.2f * (work > stream ? stream : work);
+      if (splits > 1) us += 1.5f + 1.7e-6f * splits * M * m;
+      if (us < least) {
+        least = us;
+        best = {shape, splits};
+      }
+    }
+  }
+  return best;
+}
+
+size_t int8_partial_bytes(int M, int m, int n) {
+  const Int8Plan p = int8_plan(M, m, n, 0);
+  if (p.splits <= 1) return 0;
+  const TileCost& t = kTiles[p.shape];
+  return (size_t)((m + t.out - 1) / t.out) * ((M + t.rows - 1) / t.rows) * p.splits * t.out * t.rows * 4;
+}
+
+hipError_t launch_int8_gemm(const Int8Args& args, hipStream_t s) {
+  Int8Args a = args;
+  const Int8Plan p = int8_plan(a.M, a.m, a.n, a.offsets ? a.experts : 0);
+  a.splits = p.splits;
+  switch (p.shape) {
+    case 0: return launch_shape<TileShape<4, 8, 4, 2, 128, 2, 1>>(a, s);
+    case 1: return launch_shape<TileShape<4, 4, 4, 2, 128, 3>>(a, s);
+    case 2: return launch_shape<TileShape<4, 4, 4, 2, 64, 3, 0, 4>>(a, s);
+    case 3: return launch_shape<TileShape<2, 4, 4, 2, 128, 3>>(a, s);
+    case 4: return launch_shape<TileShape<2, 4, 4, 1, 128, 3>>(a, s);
+    case 5: return launch_shape<TileShape<1, 2, 4, 1, 256, 3>>(a, s);
+    case 6: return launch_shape<TileShape<1, 1, 2, 1, 512, 3>>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace tg

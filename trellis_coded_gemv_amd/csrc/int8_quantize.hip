@@ -1,10 +1,6 @@
-// 8-bit integer rows and products: a quantiser with a scale for each row, and
-// Y[r, o] = (sum_i xq[r, i] wq[o, i]) * xs[r] * ws[o] for a dense layer and for the experts of routed pairs.
-//
-// The sums are exact in int32 (|q| <= 128 and n < 2^17, so no sum leaves the type), whatever the order and the
-// split of the work; one output is rounded three times in binary32 (the sum, and its product with either scale),
-// and once more to a 16-bit output type.
-#include "tg_int8.hpp"
+// 8-bit rows with a scale for each row.
+#include "tg_device.hpp"
+#include "tg_internal.hpp"
 
 namespace tg {
 
@@ -176,125 +172,6 @@ hipError_t launch_int8_quantize(int rows, int n, const void* x, int dtype, int64
   if (dtype == kF32) return launch_quantize_t<kF32>(rows, n, x, ldx, q, ldq, scales, s);
   if (dtype == kF16) return launch_quantize_t<kF16>(rows, n, x, ldx, q, ldq, scales, s);
   return launch_quantize_t<kBf16>(rows, n, x, ldx, q, ldq, scales, s);
-}
-
-// ---------------------------------------------------------------------------
-// Products. The layer's rows are the A operand of v_mfma_i32_16x16x64_i8 and the activation rows the B operand, so a
-// lane ends with four neighbouring outputs of one activation row. Lane l supplies row l % 16 and the 16 bytes at
-// 16 * (l / 16) of a 64-byte step on both sides.
-// ---------------------------------------------------------------------------
-
-// A workgroup of 8 waves owns 16*OT outputs and 16*RT activation rows; its waves share out the inner axis in blocks
-// of 256 bytes and are summed through LDS at the end.
-template <int RT, int OT, int DT>
-__global__ __launch_bounds__(512) void int8_rows_kernel(const Int8Args a) {
-  __shared__ i32x4 red[8][OT * RT][64];
-  const int lane = threadIdx.x & 63, wave = wave_id();
-  const int j = lane & 15, g = lane >> 4;
-  const int o0 = blockIdx.x * 16 * OT;
-  const RowTile tile = find_tile(a, blockIdx.y, 16 * RT);
-  if (tile.count <= 0) return;
-  const int8_t* wp[OT];
-  const int8_t* xp[RT];
-#pragma unroll
-  for (int t = 0; t < OT; ++t) wp[t] = a.w + ((int64_t)tile.expert * a.m + min(o0 + 16 * t + j, a.m - 1)) * a.ldw + 16 * g;
-#pragma unroll
-  for (int r = 0; r < RT; ++r) xp[r] = a.x + (int64_t)(max(pair_of(a, tile, 16 * r + j), 0) / a.pairs_per_row) * a.ldx + 16 * g;
-  i32x4 acc[OT][RT];
-#pragma unroll
-  for (int t = 0; t < OT; ++t)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) acc[t][r] = i32x4{0, 0, 0, 0};
-  const int nb = a.n >> 8;
-  for (int b = wave; b < nb; b += 8) {
-    i32x4 wv[4][OT], xv[4][RT];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-#pragma unroll
-      for (int t = 0; t < OT; ++t) wv[u][t] = *reinterpret_cast<const i32x4*>(wp[t] + b * 256 + u * 64);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) xv[u][r] = *reinterpret_cast<const i32x4*>(xp[r] + b * 256 + u * 64);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int t = 0; t < OT; ++t)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[t][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u][t], xv[u][r], acc[t][r], 0, 0, 0);
-  }
-  if (wave == (nb & 7)) {   // the rest of the inner axis, below 256 bytes: 16-byte pieces past its end count as zero
-    for (int k = nb * 256; k < a.n; k += 64) {
-      const bool in = k + 16 * g < a.n;
-      i32x4 wv[OT], xv[RT];
-#pragma unroll
-      for (int t = 0; t < OT; ++t) wv[t] = in ? *reinterpret_cast<const i32x4*>(wp[t] + k) : i32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int r = 0; r < RT; ++r) xv[r] = in ? *reinterpret_cast<const i32x4*>(xp[r] + k) : i32x4{0, 0, 0, 0};
-#pragma unroll
-      for (int t = 0; t < OT; ++t)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[t][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[t], xv[r], acc[t][r], 0, 0, 0);
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < OT; ++t)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) red[wave][t * RT + r][lane] = acc[t][r];
-  __syncthreads();
-  for (int i = threadIdx.x; i < OT * RT * 64; i += 512) {
-    const int tr = i >> 6, l = i & 63;
-    i32x4 sum = red[0][tr][l];
-#pragma unroll
-    for (int w = 1; w < 8; ++w) sum += red[w][tr][l];
-    const int t = tr / RT, r = tr % RT;
-    const int p = pair_of(a, tile, 16 * r + (l & 15));
-    const int o = o0 + 16 * t + 4 * (l >> 4);
-    if (p < 0 || o >= a.m) continue;
-    const float xs = a.xs[p / a.pairs_per_row];
-    float v[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = (float)sum[c] * xs * a.ws[(int64_t)tile.expert * a.m + min(o + c, a.m - 1)];
-    store4<DT>(a.y, (int64_t)p * a.ldy + o, v, a.m - o, a.wide_y);
-  }
-}
-
-template <int RT, int OT>
-static hipError_t launch_rows(const Int8Args& a, int tiles, hipStream_t s) {
-  const dim3 grid((unsigned)((a.m + 16 * OT - 1) / (16 * OT)), (unsigned)tiles), block(512);
-  if (a.out == kF32) hipLaunchKernelGGL((int8_rows_kernel<RT, OT, kF32>), grid, block, 0, s, a);
-  else if (a.out == kF16) hipLaunchKernelGGL((int8_rows_kernel<RT, OT, kF16>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((int8_rows_kernel<RT, OT, kBf16>), grid, block, 0, s, a);
-  return hipGetLastError();
-}
-
-// Outputs and rows of the tile shapes of int8_tile.hip.
-struct TileSize {
-  int out, rows;
-};
-constexpr TileSize kTiles[] = {{256, 256}, {128, 128}, {128, 64}, {128, 32}, {256, 256}, {256, 128}, {128, 128}, {256, 128}, {128, 128}, {256, 128}, {128, 256}, {64, 64}, {256,128},{128,128},{128,128},{128,128},{256,128},{256,128},{128,64},{128,32},{64,64},{64,32},{128,32}};
-
-Int8Plan int8_plan(int M, int m, int n, int experts) {
-  const int avg = experts > 0 ? (M + experts - 1) / experts : M;
-  if (avg <= 16) return {-1, 1};
-  if (avg <= 32) return {3, 1};
-  if (avg <= 64) return {2, 1};
-  if (avg <= 128) return {1, 1};
-  return {0, 1};
-}
-
-size_t int8_partial_bytes(int M, int m, int n) {
-  const Int8Plan p = int8_plan(M, m, n, 0);
-  if (p.splits <= 1) return 0;
-  const TileSize t = kTiles[p.shape];
-  return (size_t)((m + t.out - 1) / t.out) * ((M + t.rows - 1) / t.rows) * p.splits * t.out * t.rows * 4;
-}
-
-hipError_t launch_int8_gemm(const Int8Args& args, hipStream_t s) {
-  Int8Args a = args;
-  const Int8Plan p = int8_plan(a.M, a.m, a.n, a.offsets ? a.experts : 0);
-  a.splits = p.splits;
-  if (p.shape >= 0) return launch_int8_tile(a, p.shape, s);
-  return launch_rows<1, 1>(a, row_tiles(a, 16), s);
 }
 
 }  // namespace tg

@@ -145,7 +145,7 @@ struct RouteArgs {
 hipError_t launch_moe_route(const RouteArgs& a, int dtype, hipStream_t s);
 hipError_t launch_moe_group(int pairs, int experts, const int32_t* sel, int32_t* offsets, int32_t* order, hipStream_t s);
 
-// 8-bit products (int8.hip): dense, or the experts of routed pairs when offsets is set.
+// 8-bit rows (int8_quantize.hip) and products (int8_gemm.hip): dense, or the experts of routed pairs when offsets is set.
 struct Int8Args {
   const int8_t* x;
   const float* xs;
@@ -165,7 +165,7 @@ struct Int8Args {
 };
 // The kernel and the split of the inner axis that a product takes.
 struct Int8Plan {
-  int shape;              // -1: rows straight to registers; else a tile shape of int8_tile.hip
+  int shape;              // a tile shape of int8_gemm.hip
   int splits;
 };
 Int8Plan int8_plan(int M, int m, int n, int experts);   // experts 0: a dense product

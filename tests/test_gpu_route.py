@@ -120,7 +120,7 @@ def test_close_scores_are_decided_in_64_bits():
 
 
 @pytest.mark.parametrize("tokens,experts,top_k", [(1, 1, 1), (1, 128, 8), (64, 128, 8), (7, 3, 3), (1000, 60, 5), (4099, 257, 7),
-                                                  (16384, 256, 8), (3, 1024, 64)])
+                                                  (16384, 256, 8), (3, 1024, 64), (20000, 33, 8), (33000, 7, 4)])
 def test_group_matches_oracle(tokens, experts, top_k):
     dev = device()
     import torch

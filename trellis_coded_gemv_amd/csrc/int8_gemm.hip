@@ -18,17 +18,6 @@ namespace tg {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
-// Sum over the lanes up to this one.
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast 15 to rows 1 and 3, 31 to rows 2 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
-  return v;
-}
-
 // A workgroup's tile. rows: dense, output rows first .. first + count - 1; experts, places first .. of order.
 struct Tile {
   int ot, rt, sp;             // output tile, row tile, part of the inner axis

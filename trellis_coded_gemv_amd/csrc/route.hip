@@ -247,41 +247,48 @@ __global__ __launch_bounds__(1024) void group_kernel(const int32_t* __restrict__
     }
   };
   uint32_t kept[kGroupSteps / 8] = {};                          // four bits per step: this lane's hits
-  int less = 0, same = 0;
+  int less = 0, same = 0;                                       // of the wave
   auto count = [&](const uint32_t(&id)[4]) {
     uint32_t hits = 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      less += id[c] < mine ? 1 : 0;
+      less += __popcll(__ballot(id[c] < mine));
       hits |= id[c] == mine ? 1u << c : 0u;
     }
-    same += __popc(hits);
     return hits;
   };
   if constexpr (KEEP) {
 #pragma unroll
     for (int b = 0; b < kGroupSteps / 8; ++b) {
       if (8 * b >= steps) break;
-      uint32_t id[8][4];
+      if (wide && 8 * b + 8 <= steps && wave * steps * 256 + (8 * b + 8) * 256 <= pairs) {
+        u32x4 v[8];                                             // eight loads in flight
 #pragma unroll
-      for (int i = 0; i < 8; ++i) load(8 * b + i, id[i]);       // past the wave's stretch: the next one's, masked below
+        for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4*>(sel + begin + (8 * b + i) * 256);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (8 * b + i >= steps) break;
-        kept[b] |= count(id[i]) << (4 * i);
+        for (int i = 0; i < 8; ++i) {
+          uint32_t id[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) id[c] = min(v[i][c], (uint32_t)experts);
+          kept[b] |= count(id) << (4 * i);
+        }
+      } else {
+        for (int i = 0; i < 8 && 8 * b + i < steps; ++i) {
+          uint32_t id[4];
+          load(8 * b + i, id);
+          kept[b] |= count(id) << (4 * i);
+        }
       }
+      same += __popc(kept[b]);
     }
   } else {
     for (int i = 0; i < steps; ++i) {
       uint32_t id[4];
       load(i, id);
-      count(id);
+      same += __popc(count(id));
     }
   }
-  for (int m = 32; m; m >>= 1) {
-    less += __shfl_xor(less, m, 64);
-    same += __shfl_xor(same, m, 64);
-  }
+  same = __builtin_amdgcn_readlane(wave_scan(same), 63);
   if (lane == 0) {
     less_sh[wave] = less;
     same_sh[wave] = same;
@@ -293,25 +300,35 @@ __global__ __launch_bounds__(1024) void group_kernel(const int32_t* __restrict__
     if (w < wave) at += same_sh[w];
   }
   if (threadIdx.x == 0) offsets[mine] = base;                   // offsets[experts]: the pairs with an expert
+  if (same == 0) return;
   at += base;
-  if (__builtin_amdgcn_readfirstlane(same) == 0) return;
-  auto write = [&](int step, uint32_t hits) {
-    if (__ballot(hits != 0) == 0) return;
-    int before = at;                                            // hits of the lanes before this one
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const uint64_t b = __ballot((hits >> c) & 1);
-      before += __builtin_amdgcn_mbcnt_hi((uint32_t)(b >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)b, 0));
-      at += __popcll(b);
+  auto put = [&](int step, uint32_t hits, int to) {             // this lane's hits of a step
+    while (hits) {
+      order[to++] = begin + step * 256 + __builtin_ctz(hits);
+      hits &= hits - 1;
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if ((hits >> c) & 1) order[before++] = begin + step * 256 + c;
   };
   if constexpr (KEEP) {
 #pragma unroll
-    for (int b = 0; b < kGroupSteps / 8; ++b)
-      for (int i = 0; i < 8; ++i) write(8 * b + i, (kept[b] >> (4 * i)) & 15u);
+    for (int b = 0; b < kGroupSteps / 8; ++b) {
+      if (8 * b >= steps || __ballot(kept[b] != 0) == 0) continue;
+      // The lanes' hits of eight steps, summed over the lanes at once: ten bits hold the at most 256 hits of a step.
+      int mine3[3], upto[3], total[3];
+#pragma unroll
+      for (int d = 0; d < 3; ++d) {
+        mine3[d] = 0;
+#pragma unroll
+        for (int i = 0; i < 3 && 3 * d + i < 8; ++i) mine3[d] |= __popc((kept[b] >> (4 * (3 * d + i))) & 15u) << (10 * i);
+        upto[d] = wave_scan(mine3[d]);
+        total[d] = __builtin_amdgcn_readlane(upto[d], 63);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d = i / 3, sh = 10 * (i % 3);
+        put(8 * b + i, (kept[b] >> (4 * i)) & 15u, at + (((upto[d] - mine3[d]) >> sh) & 1023));
+        at += (total[d] >> sh) & 1023;
+      }
+    }
   } else {
     for (int i = 0; i < steps; ++i) {
       uint32_t id[4];
@@ -319,7 +336,9 @@ __global__ __launch_bounds__(1024) void group_kernel(const int32_t* __restrict__
       uint32_t hits = 0;
 #pragma unroll
       for (int c = 0; c < 4; ++c) hits |= id[c] == mine ? 1u << c : 0u;
-      write(i, hits);
+      const int n = __popc(hits), upto = wave_scan(n);
+      put(i, hits, at + upto - n);
+      at += __builtin_amdgcn_readlane(upto, 63);
     }
   }
 }

@@ -23,6 +23,47 @@ __device__ __forceinline__ float wave_max_f32(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+#define TG_STEP(ctrl) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, 0xF, 0xF, true));
+  TG_STEP(0x111) TG_STEP(0x112) TG_STEP(0x114) TG_STEP(0x118) TG_STEP(0x142) TG_STEP(0x143)
+#undef TG_STEP
+  return __builtin_amdgcn_readlane((int)v, 63);
+}
+
+__device__ __forceinline__ float wave_sum_f32(float v) {
+#define TG_STEP(ctrl, rows)                                                                                        \
+  v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), ctrl, rows, 0xF, false));
+  TG_STEP(0x111, 0xF) TG_STEP(0x112, 0xF) TG_STEP(0x114, 0xF) TG_STEP(0x118, 0xF) TG_STEP(0x142, 0xA) TG_STEP(0x143, 0xC)
+#undef TG_STEP
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// Numbers as words of the same order; none is 0.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, f + 0.0f);   // -0 and +0 are equal
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t w) {
+  return __builtin_bit_cast(float, w & 0x80000000u ? w ^ 0x80000000u : ~w);
+}
+
+// The two largest of what it takes; T's least value stands for "none".
+template <class T>
+struct Best2 {
+  T first, second;
+  __device__ __forceinline__ explicit Best2(T none) : first(none), second(none) {}
+  __device__ __forceinline__ static T larger(T a, T b) { return a > b ? a : b; }
+  __device__ __forceinline__ static T smaller(T a, T b) { return a > b ? b : a; }
+  __device__ __forceinline__ void take(T v) {
+    second = larger(second, smaller(first, v));
+    first = larger(first, v);
+  }
+  __device__ __forceinline__ void take(T f, T s) {           // another's two
+    second = larger(larger(second, s), smaller(first, f));
+    first = larger(first, f);
+  }
+};
+
 __device__ __forceinline__ double lane_value(double v, int lane) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
   const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane), hi = __builtin_amdgcn_readlane((int)(b >> 32), lane);
@@ -30,8 +71,17 @@ __device__ __forceinline__ double lane_value(double v, int lane) {
 }
 
 __device__ __forceinline__ double wave_sum(double v) {
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m, 64);
-  return v;
+  double lane63 = v;
+#define TG_STEP(ctrl, rows)                                                                                        \
+  {                                                                                                                \
+    const uint64_t b = __builtin_bit_cast(uint64_t, lane63);                                                       \
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, ctrl, rows, 0xF, false);                  \
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), ctrl, rows, 0xF, false);                    \
+    lane63 += __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);                                                 \
+  }
+  TG_STEP(0x111, 0xF) TG_STEP(0x112, 0xF) TG_STEP(0x114, 0xF) TG_STEP(0x118, 0xF) TG_STEP(0x142, 0xA) TG_STEP(0x143, 0xC)
+#undef TG_STEP
+  return lane_value(lane63, 63);
 }
 
 // What the lanes of a wave wrote to LDS is seen by its other lanes.
@@ -48,15 +98,53 @@ __device__ __forceinline__ float logit(const void* p, int64_t i) {
   return __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
 constexpr int kRouteWaves = 4;   // tokens of a workgroup where there are many
 
 }  // namespace
 
+// The two largest keys of group g in lane g, from every expert's. Where a lane's experts lie in one group, each lane
+// leaves its own two largest and lane g goes over its group's lanes; else over its group's experts.
+template <int V, class T>
+__device__ __forceinline__ Best2<T> group_best(const T (&key)[V], T none, T* mine, int lane, int size, int n_group) {
+  Best2<T> best(none);
+  if (V > 1 && size % V == 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) best.take(key[i]);
+    mine[2 * lane] = best.first;
+    mine[2 * lane + 1] = best.second;
+    wave_lds_fence();
+    best = Best2<T>(none);
+    if (lane < n_group)
+      for (int i = 0; i < size / V; ++i)
+        best.take(mine[2 * (lane * (size / V) + i)], mine[2 * (lane * (size / V) + i) + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine[lane * V + i] = key[i];
+    wave_lds_fence();
+    if (lane < n_group)
+      for (int i = 0; i < size; ++i) best.take(mine[lane * size + i]);
+  }
+  wave_lds_fence();                                         // before the place is written again
+  return best;
+}
+
 // One wave per token; lane l holds the V neighbouring experts l V .. l V + V - 1, so that the order of lanes is the
 // order of experts.
+//
+// The ids are those of binary64 scores, but few comparisons need them: without a bias the keys are the logits themselves,
+// and with one the scores are formed in binary32, off by less than 2^-19 (exp and 1/x of the hardware, a unit in the last
+// place each, of an argument rounded once: s (1 - s) |l| < 1/4 bounds what that costs a sigmoid, p |ln p| < 0.4 a
+// softmax; its sum of up to 22 terms in a row is off by less than 2^-19.5 relative). Keys further apart than two of these
+// are in their binary64 order; where some of those found are not (about 2 tokens in 1000 of the 256-expert case
+// measured), the experts found are put in order by their binary64 keys, which the lanes form anyway for the weights. A
+// token whose groups are not clearly apart (2 in 10000) is done in binary64 throughout.
 template <int V, int DT>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs a) {
-  __shared__ double ranked_sh[kRouteWaves][V * 64];
+  __shared__ double place[kRouteWaves][V * 64 < 128 ? 128 : V * 64];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int token = blockIdx.x * (blockDim.x >> 6) + wave;
   if (token >= a.tokens) return;
@@ -73,25 +161,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
   bool poison = false;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    poison |= l[i] != l[i] || !(bias[i] < inf) ;
+    poison |= l[i] != l[i] || !(bias[i] < inf);
     most = fmaxf(most, l[i]);
   }
-  double score[V], key[V];
-  if (a.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) score[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-  } else {
+  if (!a.sigmoid) {
     most = wave_max_f32(most);
     poison |= most == inf;
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      score[i] = l[i] == -inf ? 0.0 : exp((double)l[i] - (double)most);
-      sum += score[i];
-    }
-    sum = 1.0 / wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < V; ++i) score[i] *= sum;
   }
   if (__ballot(poison)) {   // a NaN, or an infinity that leaves no order: the first top_k ids, with weights that say so
     if (lane < a.top_k) {
@@ -100,104 +175,208 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
     }
     return;
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = l[i] == -inf || bias[i] == -inf ? kNone : score[i] + (double)bias[i];
-  if (a.n_group > 1) {
-    // A group's two largest keys. Where a lane's experts lie in one group, each lane leaves its own two largest, and
-    // lane g goes over its group's lanes; else over its group's experts.
-    const int size = a.experts / a.n_group;
-    double* mine = ranked_sh[wave];
-    double first = kNone, second = kNone;
-    auto take = [&](double v) {
-      const double low = fmin(first, v);
-      first = fmax(first, v);
-      second = fmax(second, low);
-    };
-    if (V > 1 && size % V == 0) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) take(key[i]);
-      mine[2 * lane] = first;
-      mine[2 * lane + 1] = second;
-      wave_lds_fence();
-      first = second = kNone;
-      if (lane < a.n_group)
-        for (int i = 0; i < size / V; ++i) {
-          take(mine[2 * (lane * (size / V) + i)]);
-          take(mine[2 * (lane * (size / V) + i) + 1]);
-        }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) mine[lane * V + i] = key[i];
-      wave_lds_fence();
-      if (lane < a.n_group)
-        for (int i = 0; i < size; ++i) take(mine[lane * size + i]);
-    }
-    const double value = a.group_top == 2 && second != kNone ? first + second : first;
+  const int size = a.experts / a.n_group;
+  auto there = [&](int i) { return l[i] != -inf && bias[i] != -inf; };
+  // The groups' ranks by value -> the kept ones as bits, and whether the border is wider than `tol` of the values.
+  auto keep = [&](auto value, float tol, float rel, bool& clear) {
     int before = 0;
     for (int i = 0; i < a.n_group; ++i) {
-      const double v = lane_value(value, i);
+      const auto v = lane_value(value, i);
       before += v > value || (v == value && i < lane) ? 1 : 0;
     }
-    const uint64_t kept = __ballot(lane < a.n_group && before < a.topk_group);
+    const uint64_t last = __ballot(lane < a.n_group && before == a.topk_group - 1);
+    const uint64_t next = __ballot(lane < a.n_group && before == a.topk_group);
+    if (next) {
+      const auto in = lane_value(value, __builtin_ctzll(last)), out = lane_value(value, __builtin_ctzll(next));
+      clear = out == (decltype(out))kNone || in - out > tol + rel * fabs(in);
+    }
+    return __ballot(lane < a.n_group && before < a.topk_group);
+  };
+  const int inverse = ((1 << 20) + size - 1) / size;        // e / size = e * inverse >> 20 for e < 2^10, size <= 2^10
+  const bool one_group = V == 1 || size % V == 0;           // a lane's experts lie in one group
+  auto in_kept = [&](uint64_t kept, int i) { return (kept >> (((lane * V + (one_group ? 0 : i)) * inverse) >> 20)) & 1; };
+
+  int my_id = -1, found = 0;   // lane i keeps the i-th expert found
+  bool sure = true, fuzzy = false;
+  {
+    uint32_t key[V];        // 0: not available
+    if (!a.bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      if (e < a.experts && !((kept >> (e / size)) & 1)) key[i] = kNone;
+      for (int i = 0; i < V; ++i) key[i] = there(i) ? ordered(l[i]) : 0u;
+    }
+    if (a.bias || a.n_group > 1) {
+      constexpr float kLog2e = 1.44269504088896340736f;
+      float score[V];
+      if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) score[i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * l[i]));
+      } else {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          score[i] = __builtin_amdgcn_exp2f(kLog2e * (l[i] - most));
+          sum += l[i] == -inf ? 0.f : score[i];
+        }
+        sum = __builtin_amdgcn_rcpf(wave_sum_f32(sum));
+#pragma unroll
+        for (int i = 0; i < V; ++i) score[i] *= sum;
+      }
+      uint32_t rank[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        rank[i] = there(i) ? ordered(score[i] + bias[i]) : 0u;
+        if (a.bias) key[i] = rank[i];
+      }
+      if (a.n_group > 1) {
+        const Best2<uint32_t> best = group_best<V, uint32_t>(rank, 0u, reinterpret_cast<uint32_t*>(place[wave]), lane, size, a.n_group);
+        const float value = best.first == 0 ? -inf
+                            : unordered(best.first) + (a.group_top == 2 && best.second != 0 ? unordered(best.second) : 0.f);
+        const uint64_t kept = keep(value, 0x1p-17f, 0x1p-21f, sure);
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = in_kept(kept, i) ? key[i] : 0u;
+      }
+    }
+    // A round: the wave's largest key, its first holder, one key less.
+    uint32_t my_key = 0;
+    auto largest = [&]() {
+      uint32_t m = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) m = max(m, key[i]);
+      return wave_max_u32(m);
+    };
+    auto round = [&](uint32_t top) {
+      uint64_t hit[V], any = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        hit[i] = __ballot(key[i] == top);
+        any |= hit[i];
+      }
+      const int owner = __builtin_ctzll(any);
+      int at = 0;
+#pragma unroll
+      for (int i = V - 1; i > 0; --i) at = (hit[i] >> owner) & 1 ? i : at;
+      if ((hit[0] >> owner) & 1) at = 0;
+      const int id = owner * V + at;
+      my_id = lane == found ? id : my_id;
+      my_key = lane == found ? top : my_key;
+      ++found;
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = lane == (i == at ? owner : -1) ? 0u : key[i];
+    };
+    uint32_t top = 0;
+    while (sure && found < a.top_k) {
+      top = largest();
+      if (top == 0) break;  // no expert is left: the other slots stay -1 with weight 0
+      round(top);
+    }
+    if (a.bias && sure && found > 0) {
+      // Rounds go on past the top_k-th until the next key is clearly smaller; two keys that are not clearly apart leave
+      // the order to binary64.
+      auto apart = [](float x, float y) { return x - y > 0x1p-18f + 0x1p-22f * fabsf(y); };
+      uint32_t beyond = 0;
+      for (;;) {
+        beyond = found < a.top_k ? 0u : largest();
+        if (beyond == 0 || apart(unordered(__builtin_amdgcn_readlane((int)my_key, found - 1)), unordered(beyond))) break;
+        if (found == 64) {
+          sure = false;     // more of them than lanes
+          break;
+        }
+        round(beyond);
+      }
+      const uint32_t after = __shfl_down((int)my_key, 1, 64);
+      fuzzy = __ballot(lane + 1 < found && !apart(unordered(my_key), unordered(after))) != 0;
     }
   }
-  if (!a.bias) {            // the same order as the scores', without their rounding
+  if (!sure) {              // in binary64 throughout
+    double score[V], key[V];
+    if (a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = key[i] == kNone ? kNone : (double)l[i];
-  }
-  // top_k rounds: each lane's largest key, and the wave's by its binary32 rounding, which keeps the order; only where
-  // several lanes share the largest rounding are their keys compared in full.
-  int my_id = -1;           // lane i keeps slot i
-  double my_w = 0.0;
-  for (int s = 0; s < a.top_k; ++s) {
-    double best = key[0], w = score[0];
-    int at = 0;
+      for (int i = 0; i < V; ++i) score[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+    } else {
+      double sum = 0.0;
 #pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i;
-        w = score[i];
+      for (int i = 0; i < V; ++i) {
+        score[i] = l[i] == -inf ? 0.0 : exp((double)l[i] - (double)most);
+        sum += score[i];
       }
-    const float near = (float)best;
-    const float top = wave_max_f32(near);
-    if (top == -inf) break;   // no expert is left: the other slots stay -1 with weight 0
-    uint64_t mask = __ballot(near == top);
-    int owner = __builtin_ctzll(mask);
-    mask &= mask - 1;
-    if (mask) {
+      sum = 1.0 / wave_sum(sum);
+#pragma unroll
+      for (int i = 0; i < V; ++i) score[i] *= sum;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = there(i) ? score[i] + (double)bias[i] : kNone;
+    uint64_t kept = ~0ull;
+    if (a.n_group > 1) {
+      bool clear;
+      const Best2<double> best = group_best<V, double>(key, kNone, place[wave], lane, size, a.n_group);
+      kept = keep(a.group_top == 2 && best.second != kNone ? best.first + best.second : best.first, 0.f, 0.f, clear);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (!a.bias && there(i)) key[i] = l[i];               // the scores' order, without their rounding
+      if (a.n_group > 1 && !in_kept(kept, i)) key[i] = kNone;
+    }
+    my_id = -1;
+    fuzzy = false;
+    for (int s = 0; s < a.top_k; ++s) {
+      double best = key[0];
+      int at = 0;
+#pragma unroll
+      for (int i = 1; i < V; ++i)
+        if (key[i] > best) {
+          best = key[i];
+          at = i;
+        }
+      const float near = (float)best;                       // keeps the order; equal ones are compared in full
+      const float top = wave_max_f32(near);
+      if (top == -inf) break;
+      uint64_t mask = __ballot(near == top);
+      int owner = __builtin_ctzll(mask);
       double most_key = lane_value(best, owner);
-      while (mask) {
+      for (mask &= mask - 1; mask; mask &= mask - 1) {
         const int o = __builtin_ctzll(mask);
-        mask &= mask - 1;
         const double k = lane_value(best, o);
         if (k > most_key) {
           most_key = k;
           owner = o;
         }
       }
-    }
-    const int id = owner * V + __builtin_amdgcn_readlane(at, owner);
-    const double sw = lane_value(w, owner);
-    if (lane == s) {
-      my_id = id;
-      my_w = sw;
-    }
+      const int id = owner * V + __builtin_amdgcn_readlane(at, owner);   // read with every lane active
+      my_id = lane == s ? id : my_id;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane == owner && i == at) key[i] = kNone;
+      for (int i = 0; i < V; ++i)
+        if (lane == owner && i == at) key[i] = kNone;
+    }
+  }
+  double w = 0.0, total = 0.0;
+  if (my_id >= 0) {
+    const double ml = logit<DT>(a.logits, at0 + my_id);
+    w = a.sigmoid ? 1.0 / (1.0 + exp(-ml)) : exp(ml - (double)most);
+  }
+  if (!a.sigmoid && (fuzzy || !a.renorm)) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) total += l[i] == -inf ? 0.0 : exp((double)l[i] - (double)most);
+    total = wave_sum(total);
+    w = my_id >= 0 ? w / total : 0.0;
+  }
+  int slot = lane;
+  if (fuzzy) {              // those found, by their binary64 keys
+    const double key = my_id >= 0 ? w + (double)a.bias[my_id] : kNone;
+    int before = 0;
+    for (int i = 0; i < found; ++i) {
+      const double k = lane_value(key, i);
+      const int id = __builtin_amdgcn_readlane(my_id, i);
+      before += k > key || (k == key && id < my_id) ? 1 : 0;
+    }
+    slot = lane < found ? before : lane;
   }
   if (a.renorm) {
-    const double total = wave_sum(my_w);
-    my_w = total > 0.0 ? my_w / total : 0.0;
+    total = wave_sum(slot < a.top_k ? w : 0.0);
+    w = total > 0.0 ? w / total : 0.0;
   }
-  if (lane < a.top_k) {
-    a.sel[(int64_t)token * a.top_k + lane] = my_id;
-    a.weights[(int64_t)token * a.top_k + lane] = (float)(my_w * (double)a.scale);
+  if (slot < a.top_k) {
+    a.sel[(int64_t)token * a.top_k + slot] = my_id;
+    a.weights[(int64_t)token * a.top_k + slot] = (float)(w * (double)a.scale);
   }
 }
 

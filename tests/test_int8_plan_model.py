@@ -108,10 +108,11 @@ def test_every_tile_is_found_once(out_tiles, row_tiles, splits):
 @pytest.mark.parametrize("case", range(7))
 def test_lds_rows_cover_the_outputs(case):
     at, _, wo = shapes()[1][case][:3]
-    outs = [q // (16 * at) * (16 * at) + 4 * at * ((q >> 2) & 3) + 4 * ((q >> 4) % at) + (q & 3) for q in range(16 * at * wo)]
+    output = lambda t, g: 4 * g if at == 1 else 32 * (t // 2) + 8 * g + 4 * (t % 2)
+    outs = [q // (16 * at) * (16 * at) + output((q >> 4) % at, (q >> 2) & 3) + (q & 3) for q in range(16 * at * wo)]
     assert sorted(outs) == list(range(16 * at * wo))
-    for w in range(wo):                                      # lane group g, tile t, register v of a wave
-        for t in range(at):
-            for g in range(4):
-                for v in range(4):
-                    assert outs[16 * (at * w + t) + 4 * g + v] == 16 * at * w + 4 * at * g + 4 * t + v
+    for w in range(wo):                                      # a lane (group g) of a wave stores eight neighbours at once
+        for g in range(4):
+            for t in range(0, at - 1, 2):
+                mine = [outs[16 * (at * w + u) + 4 * g + v] for u in (t, t + 1) for v in range(4)]
+                assert mine == list(range(mine[0], mine[0] + 8)) and mine[0] % 8 == 0

@@ -471,10 +471,12 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int
     torch = _torch()
     w = "moe_route"
     dtype = _dtype_code(logits.dtype, w)
-    _expect(logits.dim() == 2, w, "expected logits [tokens, experts]")
+    if logits.dim() != 2:
+        raise ValueError(f"{w}: expected logits [tokens, experts]")
     tokens, experts = logits.shape
     ld, inner = logits.stride()
-    _expect(inner == 1 or experts == 1, w, "a token's logits have to be neighbours")
+    if inner != 1 and experts != 1:
+        raise ValueError(f"{w}: a token's logits have to be neighbours")
     if bias is not None:
         _expect(bias.dtype == torch.float32 and bias.shape == (experts,) and bias.is_contiguous(), w, f"expected a float32 bias [{experts}]")
     at = _common_device(w, logits, bias, sel, weights)
@@ -482,11 +484,11 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int
         with _Entered(at, stream):
             return moe_route(logits, top_k, bias, sigmoid, n_group, topk_group, group_top, renormalize, scale, sel, weights)
     if sel is None:
-        sel = logits.new_empty((tokens, top_k), dtype=torch.int32)
+        sel = torch.empty(tokens, top_k, dtype=torch.int32, device=logits.device)
     else:
         _expect(sel.dtype == torch.int32 and sel.shape == (tokens, top_k) and sel.is_contiguous(), w, f"expected sel int32 [{tokens}, {top_k}]")
     if weights is None:
-        weights = logits.new_empty((tokens, top_k), dtype=torch.float32)
+        weights = torch.empty(tokens, top_k, dtype=torch.float32, device=logits.device)
     else:
         _expect(weights.dtype == torch.float32 and weights.shape == (tokens, top_k) and weights.is_contiguous(), w,
                 f"expected weights float32 [{tokens}, {top_k}]")
@@ -501,19 +503,20 @@ def moe_group(sel, experts: int, offsets=None, order=None, stream=None):
     int32 ids of any shape; the pairs whose id is no expert come last, behind offsets[experts]."""
     torch = _torch()
     w = "moe_group"
-    _expect(sel.dtype == torch.int32 and sel.is_contiguous(), w, "expected contiguous int32 ids")
+    if sel.dtype != torch.int32 or not sel.is_contiguous():
+        raise ValueError(f"{w}: expected contiguous int32 ids")
     pairs = sel.numel()
     at = _common_device(w, sel, offsets, order)
     if _elsewhere(torch, at, stream):
         with _Entered(at, stream):
             return moe_group(sel, experts, offsets, order)
     if offsets is None:
-        offsets = sel.new_empty(experts + 1)
+        offsets = torch.empty(experts + 1, dtype=torch.int32, device=sel.device)
     else:
         _expect(offsets.dtype == torch.int32 and offsets.shape == (experts + 1,) and offsets.is_contiguous(), w,
                 f"expected offsets int32 [{experts + 1}]")
     if order is None:
-        order = sel.new_empty(pairs)
+        order = torch.empty(pairs, dtype=torch.int32, device=sel.device)
     else:
         _expect(order.dtype == torch.int32 and order.shape == (pairs,) and order.is_contiguous(), w, f"expected order int32 [{pairs}]")
     _check(lib().moe_group(pairs, experts, sel.data_ptr(), offsets.data_ptr(), order.data_ptr(), _current(torch, at)), w)
@@ -526,7 +529,8 @@ def int8_quantize(x, q=None, scales=None, stream=None):
     w = "int8_quantize"
     dtype = _dtype_code(x.dtype, w)
     shape = x.shape
-    _expect(len(shape) >= 1 and x.numel() > 0, w, "expected rows [..., n]")
+    if len(shape) < 1 or x.numel() == 0:
+        raise ValueError(f"{w}: expected rows [..., n]")
     at = _common_device(w, x, q, scales)
     if _elsewhere(torch, at, stream):
         with _Entered(at, stream):
@@ -539,14 +543,14 @@ def int8_quantize(x, q=None, scales=None, stream=None):
         ldx = n
     rows, ldq = x2.shape[0], n
     if q is None:
-        q = x2.new_empty(shape, dtype=torch.int8)
+        q = torch.empty(*shape, dtype=torch.int8, device=x.device)
     else:
         _expect(q.dtype == torch.int8 and q.shape == shape and (q.is_contiguous() or (q.dim() == 2 and q.stride(1) == 1 and q.stride(0) >= n)),
                 w, "expected q int8 in the shape of x, with neighbouring values")
         if q.dim() == 2 and rows > 1:
             ldq = q.stride(0)
     if scales is None:
-        scales = x2.new_empty(lead, dtype=torch.float32)
+        scales = torch.empty(lead, dtype=torch.float32, device=x.device)
     else:
         _expect(scales.dtype == torch.float32 and scales.shape == lead and scales.is_contiguous(), w, "expected a float32 scale for each row")
     _check(lib().int8_quantize(rows, n, x2.data_ptr(), dtype, ldx if rows > 1 else n, q.data_ptr(), ldq, scales.data_ptr(),
@@ -601,11 +605,14 @@ def int8_workspace(layer: "Int8Layer", M: int):
 
 
 def _int8_rows(torch, where: str, n: int, xq, xs):
-    _expect(xq.dtype == torch.int8 and xq.dim() == 2, where, f"expected xq int8 [rows, {n}]")
+    if xq.dtype != torch.int8 or xq.dim() != 2:
+        raise ValueError(f"{where}: expected xq int8 [rows, {n}]")
     rows, width = xq.shape
     ldx, inner = xq.stride()
-    _expect(width == n and inner == 1, where, f"expected xq int8 [rows, {n}] with neighbouring values")
-    _expect(xs.dtype == torch.float32 and xs.shape == (rows,) and xs.is_contiguous(), where, "expected a float32 scale for each row of xq")
+    if width != n or inner != 1:
+        raise ValueError(f"{where}: expected xq int8 [rows, {n}] with neighbouring values")
+    if xs.dtype != torch.float32 or xs.shape != (rows,) or not xs.is_contiguous():
+        raise ValueError(f"{where}: expected a float32 scale for each row of xq")
     return rows, (ldx if rows > 1 else n)
 
 
@@ -613,7 +620,7 @@ def _int8_out(torch, where: str, Y, rows: int, m: int, out_dtype, xq):
     if Y is None:
         dtype = torch.float32 if out_dtype is None else out_dtype
         code = _dtype_code(dtype, where)
-        return xq.new_empty((rows, m), dtype=dtype), code, m
+        return torch.empty(rows, m, dtype=dtype, device=xq.device), code, m
     code = _dtype_code(Y.dtype, where)
     _expect(out_dtype is None or out_dtype == Y.dtype, where, "Y is not of out_dtype")
     _expect(Y.shape == (rows, m) and (Y.stride(1) == 1 or m == 1) and (rows == 1 or Y.stride(0) >= m), where, f"expected Y [{rows}, {m}] with neighbouring outputs")
@@ -647,8 +654,10 @@ def int8_gemm_grouped(experts: "Int8Experts", xq, xs, offsets, order, pairs_per_
     m, n, count = experts.m, experts.n, experts.experts
     rows, ldx = _int8_rows(torch, w, n, xq, xs)
     pairs = rows * int(pairs_per_row)
-    _expect(order.dtype == torch.int32 and order.shape == (pairs,) and order.is_contiguous(), w, f"expected order int32 [{pairs}]")
-    _expect(offsets.dtype == torch.int32 and offsets.shape == (count + 1,) and offsets.is_contiguous(), w, f"expected offsets int32 [{count + 1}]")
+    if order.dtype != torch.int32 or order.shape != (pairs,) or not order.is_contiguous():
+        raise ValueError(f"{w}: expected order int32 [{pairs}]")
+    if offsets.dtype != torch.int32 or offsets.shape != (count + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"{w}: expected offsets int32 [{count + 1}]")
     at = _common_device(w, xq, xs, experts.q, offsets, order, Y)
     if _elsewhere(torch, at, stream):
         with _Entered(at, stream):

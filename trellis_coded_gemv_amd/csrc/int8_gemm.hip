@@ -128,23 +128,35 @@ __device__ __forceinline__ uint32_t half_bits(float v) {
   return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
-// Four neighbouring outputs of a row, of which `valid` exist. wide: they may be stored at once.
-template <int DT>
-__device__ __forceinline__ void store4(void* y, int64_t at, const float (&v)[4], int valid, bool wide) {
+// N (4 or 8) neighbouring outputs of a row, of which `valid` exist; wide: they may be stored 16 bytes at once (N = 8 of a
+// 16-bit type, else 4).
+template <int DT, int N>
+__device__ __forceinline__ void store_outputs(void* y, int64_t at, const float (&v)[N], int valid, int wide) {
   if constexpr (DT == kF32) {
     float* p = reinterpret_cast<float*>(y) + at;
-    if (valid >= 4 && wide) *reinterpret_cast<float4_t*>(p) = float4_t{v[0], v[1], v[2], v[3]};
-    else
-      for (int i = 0; i < 4; ++i)
+    if (valid >= N && wide >= 1) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<float4_t*>(p + i) = float4_t{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
         if (i < valid) p[i] = v[i];
+    }
   } else {
     uint16_t* p = reinterpret_cast<uint16_t*>(y) + at;
-    if (valid >= 4 && wide)
-      *reinterpret_cast<u32x2*>(p) = u32x2{half_bits<DT>(v[0]) | half_bits<DT>(v[1]) << 16,
-                                           half_bits<DT>(v[2]) | half_bits<DT>(v[3]) << 16};
-    else
-      for (int i = 0; i < 4; ++i)
-        if (i < valid) p[i] = (uint16_t)half_bits<DT>(v[i]);
+    uint32_t h[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) h[i] = half_bits<DT>(v[2 * i]) | half_bits<DT>(v[2 * i + 1]) << 16;
+    if (N == 8 && valid >= 8 && wide >= 2) {
+      *reinterpret_cast<u32x4*>(p) = u32x4{h[0], h[1], h[N / 2 - 2], h[N / 2 - 1]};
+    } else if (valid >= N && wide >= 1) {
+#pragma unroll
+      for (int i = 0; i < N / 4; ++i) *reinterpret_cast<u32x2*>(p + 4 * i) = u32x2{h[2 * i], h[2 * i + 1]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i < valid) p[i] = (uint16_t)(h[i / 2] >> (16 * (i & 1)));
+    }
   }
 }
 
@@ -200,6 +212,7 @@ struct TileShape {
   static_assert(LW * RPI * NW == TO && LX * RPI * NW == TX, "every wave loads whole instructions");
   // A row's 16-byte pieces are held in LDS in an order that depends on the row, so that the lanes which read the same
   // piece of neighbouring rows spread over the banks.
+  static __device__ __forceinline__ int output(int t, int g) { return AT == 1 ? 4 * g : 32 * (t / 2) + 8 * g + 4 * (t % 2); }
   static __device__ __forceinline__ int swizzle(int row) { return BK >= 128 ? row & 7 : (row >> 1) & 3; }
 };
 
@@ -219,7 +232,8 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
 
   // Loads: an instruction fills RPI rows of LDS; lane l the slot l % (BK / 16) of row l / (BK / 16), where the piece
   // slot ^ swizzle(row) of the row belongs. LDS row 16 (AT wo + t) + 4 g + v of the layer's side holds output
-  // 16 AT wo + 4 AT g + 4 t + v, so that a lane ends with 4 AT neighbouring outputs of a row.
+  // 16 AT wo + 32 (t / 2) + 8 g + 4 (t % 2) + v (one tile to a wave: its row's number), so that a lane ends with 8
+  // neighbouring outputs of a row and the four lanes of the row with 32.
   const int lrow = lane / (BK / 16);
   auto wrow = [&](int i) { return S::RPI * (S::LW * wave + i) + lrow; };   // LDS row of this lane in instruction i
   auto xrow = [&](int i) { return S::RPI * (S::LX * wave + i) + lrow; };
@@ -231,7 +245,7 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
 #pragma unroll
   for (int i = 0; i < S::LW; ++i) {
     const int q = wrow(i);
-    const int o = q / (16 * AT) * (16 * AT) + 4 * AT * ((q >> 2) & 3) + 4 * ((q >> 4) % AT) + (q & 3);
+    const int o = AT == 1 ? q : q / (16 * AT) * (16 * AT) + S::output((q >> 4) % AT, (q >> 2) & 3) + (q & 3);
     woff[i] = (uint32_t)min(o, a.m - 1 - o0) * (uint32_t)a.ldw;
   }
 #pragma unroll
@@ -391,21 +405,40 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
     if (threadIdx.x == 0) reset_counter(a.counters + rt * out_tiles + ot);
   }
 
-  // Lane: outputs o0 + 16 AT wo + 4 AT g + 4 t + v of row 16 RX wx + 16 r + j.
-  const int ob = o0 + 16 * AT * wo + 4 * AT * g;
+  // The scales and places of the lane's outputs first: a store could not be passed by a load.
+  const int ob = o0 + 16 * AT * wo;
+  const float* ws = a.ws + (int64_t)tile.expert * a.m;
+  float wsv[AT][4], xs[RX];
+  int pair[RX];
+#pragma unroll
+  for (int t = 0; t < AT; ++t) {
+    const int o = ob + S::output(t, g);
+    if (a.wide_ws && o < a.m) {
+      const float4_t f = *reinterpret_cast<const float4_t*>(ws + o);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) wsv[t][c] = f[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) wsv[t][c] = ws[min(o + c, a.m - 1)];
+    }
+  }
 #pragma unroll
   for (int r = 0; r < RX; ++r) {
-    const int p = pair_of(a, tile, 16 * (RX * wx + r) + j);
-    if (p < 0) continue;
-    const float xs = a.xs[p / a.pairs_per_row];
+    pair[r] = pair_of(a, tile, 16 * (RX * wx + r) + j);
+    xs[r] = a.xs[max(pair[r], 0) / a.pairs_per_row];
+  }
+  constexpr int N = AT == 1 ? 4 : 8;
 #pragma unroll
-    for (int t = 0; t < AT; ++t) {
-      const int o = ob + 4 * t;
+  for (int r = 0; r < RX; ++r) {
+    if (pair[r] < 0) continue;
+#pragma unroll
+    for (int t = 0; t < AT; t += N / 4) {
+      const int o = ob + S::output(t, g);
       if (o >= a.m) continue;
-      float v[4];
+      float v[N];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = (float)acc[t][r][c] * xs * a.ws[(int64_t)tile.expert * a.m + min(o + c, a.m - 1)];
-      store4<DT>(a.y, (int64_t)p * a.ldy + o, v, a.m - o, a.wide_y);
+      for (int c = 0; c < N; ++c) v[c] = (float)acc[t + c / 4][r][c % 4] * xs[r] * wsv[t + c / 4][c % 4];
+      store_outputs<DT, N>(a.y, (int64_t)pair[r] * a.ldy + o, v, a.m - o, a.wide_y);
     }
   }
 }

@@ -35,28 +35,18 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
   Tile t{0, 0, 0, 0, 0, 0};
   const int lane = threadIdx.x & 63;
   const int per_lane = (a.experts + 63) >> 6;
-  int b[kHeld], c[kHeld], mine = 0, scan = 0;
-  auto place = [&](int e, int& from, int& to) {
-    from = to = 0;
-    if (e < a.experts) {
-      from = min(max(a.offsets[e], 0), a.M);
-      to = max(min(max(a.offsets[e + 1], 0), a.M), from);
-    }
-  };
-  auto tiles = [&](int from, int to) { return (to - from + rows_per_tile - 1) / rows_per_tile; };
+  int at[kHeld + 1], mine = 0, scan = 0;        // where a lane's experts begin, and the one behind them
+  // Past the last expert: where it ends, so none of its own. Places are cut to [0, M].
+  auto place = [&](int e) { return min(max(a.offsets[min(e, a.experts)], 0), a.M); };
+  auto tiles = [&](int from, int to) { return to > from ? (to - from + rows_per_tile - 1) / rows_per_tile : 0; };
   if (a.offsets) {
     if (per_lane <= kHeld) {
 #pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        place(i < per_lane ? lane * per_lane + i : a.experts, b[i], c[i]);
-        mine += tiles(b[i], c[i]);
-      }
+      for (int i = 0; i <= kHeld; ++i) at[i] = place(lane * per_lane + min(i, per_lane));
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) mine += tiles(at[i], at[i + 1]);
     } else {
-      for (int i = 0; i < per_lane; ++i) {
-        int from, to;
-        place(lane * per_lane + i, from, to);
-        mine += tiles(from, to);
-      }
+      for (int i = 0; i < per_lane; ++i) mine += tiles(place(lane * per_lane + i), place(lane * per_lane + i + 1));
     }
     scan = wave_scan(mine);
     row_tiles = min(row_tiles, __builtin_amdgcn_readlane(scan, 63));
@@ -89,18 +79,17 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
   for (int i = 0; i < per_lane; ++i) {
     int from, to;
     if (per_lane <= kHeld) {
-      int bi = b[0], ci = c[0];
+      int b = at[0], c = at[1];
 #pragma unroll
       for (int h = 1; h < kHeld; ++h) {
-        bi = i == h ? b[h] : bi;
-        ci = i == h ? c[h] : ci;
+        b = i == h ? at[h] : b;
+        c = i == h ? at[h + 1] : c;
       }
-      from = __builtin_amdgcn_readlane(bi, owner);
-      to = __builtin_amdgcn_readlane(ci, owner);
+      from = __builtin_amdgcn_readlane(b, owner);
+      to = __builtin_amdgcn_readlane(c, owner);
     } else {
-      place(owner * per_lane + i, from, to);
-      from = __builtin_amdgcn_readfirstlane(from);
-      to = __builtin_amdgcn_readfirstlane(to);
+      from = __builtin_amdgcn_readfirstlane(place(owner * per_lane + i));
+      to = __builtin_amdgcn_readfirstlane(place(owner * per_lane + i + 1));
     }
     const int n = tiles(from, to);
     if (left < n) {

@@ -119,6 +119,22 @@ def test_close_scores_are_decided_in_64_bits():
     _check(torch, dev, l, 8, dict(bias=bias, n_group=8, topk_group=4, group_top=2, sigmoid=True))
 
 
+@pytest.mark.parametrize("experts,top_k,opts", [(200, 8, {}), (200, 8, dict(sigmoid=True)), (1024, 64, dict(sigmoid=True)),
+                                                (256, 64, {}), (256, 8, dict(sigmoid=True, n_group=8, topk_group=4, group_top=2))])
+def test_all_scores_close_together(experts, top_k, opts):
+    """More scores within a binary32 rounding of each other than a wave has lanes, some of them equal in binary64 too."""
+    dev = device()
+    import torch
+    say("route all close", experts, top_k, opts)
+    rng = np.random.default_rng(experts + top_k)
+    l = (np.float32(0.5) + np.float32(6e-8) * rng.integers(-8, 9, size=(20, experts))).astype(np.float32)
+    l[1] = 0.5
+    l[2, ::7] = -np.inf
+    bias = (np.float32(0.01) + np.float32(1e-9) * rng.integers(0, 3, size=experts)).astype(np.float32)
+    _check(torch, dev, l, top_k, dict(opts, bias=bias))
+    _check(torch, dev, l, top_k, dict(opts, bias=np.zeros(experts, np.float32)))
+
+
 @pytest.mark.parametrize("tokens,experts,top_k", [(1, 1, 1), (1, 128, 8), (64, 128, 8), (7, 3, 3), (1000, 60, 5), (4099, 257, 7),
                                                   (16384, 256, 8), (3, 1024, 64), (20000, 33, 8), (33000, 7, 4)])
 def test_group_matches_oracle(tokens, experts, top_k):

@@ -28,7 +28,7 @@ def plan(M, m, n, experts=0):
     f = np.float32
     reached = f(min(experts, M)) if experts else f(1)
     rows = f(M) / reached
-    stream = (reached * f(m) * f(n) + f(M) * f(n) + f(2) * f(M) * f(m)) / f(4.68e6)
+    stream = (reached * f(m) * f(n) + f(M) * f(n) + f(2) * f(M) * f(m)) / f(5.3e6)
     steps, best, least = (n + 127) // 128, (0, 1), f(3.0e38)
     for i, (out, tx, resident, alone, shared, tile) in enumerate(shapes()[0]):
         if tx > 32 and f(tx) > f(2) * rows:
@@ -47,7 +47,7 @@ def plan(M, m, n, experts=0):
                 work += (f(shared) if rest > 256 else f(alone)) * length + f(tile)
             us = max(work, stream) + f(0.2) * min(work, stream)
             if splits > 1:
-                us += f(1.5) + f(1.7e-6) * f(splits) * f(M) * f(m)
+                us += f(0.9) + f(2.1e-6) * f(splits) * f(M) * f(m)
             if us < least:
                 least, best = us, (i, splits)
     return best
@@ -71,9 +71,10 @@ def test_table_matches_the_kernels():
 def test_every_shape_is_reached():
     seen = set()
     for M in (1, 8, 33, 64, 100, 200, 300, 700, 2048, 8192):
-        for m, n in ((28672, 8192), (8192, 8192), (4096, 14336), (1024, 8192), (8192, 1024), (512, 512), (300, 20000)):
+        for m, n in ((28672, 8192), (8192, 8192), (4096, 14336), (1024, 8192), (8192, 1024), (512, 512), (300, 20000), (9000, 272)):
             seen.add(plan(M, m, n)[0])
     assert seen == set(range(7))
+    assert {plan(pairs, 1536, 2048, 128)[0] for pairs in (8, 512, 4096, 16384, 65536)} >= {1, 2, 4, 5}
     assert any(plan(M, 4096, 14336)[1] > 1 for M in (1, 61, 256))
 
 

@@ -5,6 +5,13 @@
 // work; an output is rounded three times in binary32 (the sum, and its product with either scale) and once more to a
 // 16-bit output type.
 //
+// What bounds it (MI355X, 2.2 GHz under this load): 4096 x 28672 x 8192 runs at 2530 TOP/s, 61% of what the matrix cores
+// reach on such values from registers alone (4035 TOP/s; 4900 on zeros: the card's power). With the loads to LDS alone the
+// same kernel takes 729 of 850 us, with the reads from LDS alone 323 us, so the way from L2 is next to the power what
+// holds it; 256 x 256 tiles ask least of it. The library's own 8-bit product takes 844 us there. 1 x 28672 x 8192 reads
+// 235 MB in 42 us (5.6 TB/s; a large copy moves 5.1). 8192 tokens over 128 experts, 1536 x 2048, top 8: 298 us, of which
+// the products of the partly filled tiles take about 225, first loads and lookups 42, the stores 35.
+//
 // v_mfma_i32_16x16x64_i8 with the layer's rows as its A operand and the activation rows as its B operand: lane l
 // supplies row l % 16 and the 16 bytes at 16 (l / 16) of 64 bytes of the inner axis on both sides, and ends with four
 // neighbouring outputs of row l % 16. Both sides reach LDS by loads that do not pass through registers, a ring of ST
@@ -457,20 +464,22 @@ struct TileCost {
 };
 constexpr TileCost kTiles[] = {
     {256, 256, 1, 1.80f, 1.80f, 5.6f},   // TileShape<4, 8, 4, 2, 128, 2, 1>
-    {256, 128, 1, 1.02f, 1.02f, 5.0f},   // TileShape<4, 4, 4, 2, 128, 3>
-    {256, 128, 2, 1.88f, 1.95f, 2.0f},   // TileShape<4, 4, 4, 2, 64, 3, 0, 4>: two workgroups fill each other's waits
+    {256, 128, 1, 1.02f, 1.02f, 4.3f},   // TileShape<4, 4, 4, 2, 128, 3>
+    {256, 128, 2, 1.88f, 2.27f, 2.0f},   // TileShape<4, 4, 4, 2, 64, 3, 0, 4>: two workgroups fill each other's waits
     {128, 128, 1, 0.60f, 0.60f, 2.0f},   // TileShape<2, 4, 4, 2, 128, 3>
-    {128, 64, 2, 0.35f, 0.79f, 1.4f},    // TileShape<2, 4, 4, 1, 128, 3>
+    {128, 64, 2, 0.344f, 0.79f, 1.7f},    // TileShape<2, 4, 4, 1, 128, 3>
     {64, 32, 2, 0.13f, 0.25f, 1.15f},    // TileShape<1, 2, 4, 1, 256, 3>
-    {32, 16, 2, 0.057f, 0.14f, 0.64f},   // TileShape<1, 1, 2, 1, 512, 3>
+    {32, 16, 2, 0.042f, 0.132f, 0.64f},   // TileShape<1, 1, 2, 1, 512, 3>
 };
-constexpr float kStreamRate = 4.68e6f;   // bytes per microsecond of a product that waits for memory alone
+constexpr float kStreamRate = 5.3e6f;   // bytes per microsecond of a product that waits for memory alone
 constexpr int kComputeUnits = 256;
 
 // The cheapest shape and split of the inner axis: rounds of workgroups over the compute units, and the time that the
-// bytes take, of which a part is not hidden behind the other. Against trying everything this loses 0.4% over the sweep,
-// where any one shape loses a factor of 1.3 to 20 somewhere. A split inner axis costs the parts' sums, so only products
-// with few tiles take one. Experts: row tiles as an even routing fills them, one half-filled for each expert.
+// bytes take, of which a part is not hidden behind the other. Over the sweep this loses 0.4% against trying everything
+// (12% at worst, 1.4 us of a 9 us product); the best single shape loses 22% on average and a factor of 2.1 at worst, the
+// largest tile a factor of 2.3 and 7.1. A split inner axis costs the parts' sums, so only products with few tiles take
+// one (61 x 4096 x 14336: 19.9 us whole, 14.4 us in two parts; 256 x 28672 x 8192: 76 us whole, 128 us in two).
+// Experts: row tiles as an even routing fills them, one half-filled for each expert.
 Int8Plan int8_plan(int M, int m, int n, int experts) {
   const float reached = experts > 0 ? (float)(experts < M ? experts : M) : 1.f;
   const float rows = (float)M / reached;
@@ -493,7 +502,7 @@ Int8Plan int8_plan(int M, int m, int n, int experts) {
       float work = rounds * (t.shared * len + t.tile);
       if (rest > 0.f) work += (rest > kComputeUnits ? t.shared : t.alone) * len + t.tile;
       float us = (work > stream ? work : stream) + 0.2f * (work > stream ? stream : work);
-      if (splits > 1) us += 1.5f + 1.7e-6f * splits * M * m;
+      if (splits > 1) us += 0.9f + 2.1e-6f * splits * M * m;
       if (us < least) {
         least = us;
         best = {shape, splits};

@@ -1,4 +1,5 @@
-// 8-bit rows with a scale for each row.
+// 8-bit rows with a scale for each row. Bound by memory: 4096 rows of 14336 bf16 values (117 MB in, 59 MB out) take 30
+// us, 5.9 TB/s, where a large copy moves 5.1; reading a row twice took 105 us. One row of 8192 takes 2.7 us.
 #include "tg_device.hpp"
 #include "tg_internal.hpp"
 
@@ -140,6 +141,9 @@ __global__ __launch_bounds__(THREADS) void quantize_any_kernel(const void* __res
     qr[i] = r.finite ? (int8_t)quantize_step(load_elem<DT>(x, base + i), r.inv) : (int8_t)0;
 }
 
+// A row is a workgroup's, of 256 threads where a thread then holds one 16-byte piece (4096 rows of 1024 fp16 values: 5.6
+// us, with 1024 threads 14.2), or up to four of many rows (2048 x 8192: 11.6 and 13.1), else of 1024 (1 x 8192: 2.7 and
+// 3.1; 4096 x 14336: 30 and 48).
 template <int DT, int THREADS>
 static void launch_quantize_rows(int rows, int n, const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scales,
                                  hipStream_t s) {
@@ -160,7 +164,7 @@ static hipError_t launch_quantize_t(int rows, int n, const void* x, int64_t ldx,
                        (rows == 1 || (ldx % VEC == 0 && ldq % VEC == 0));
   const int pieces = n / VEC;
   if (aligned && pieces <= 256 && pieces >= 1) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
-  else if (aligned && pieces <= 8 * 256 && rows > 512) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
+  else if (aligned && pieces <= 4 * 256 && rows >= 512) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
   else if (aligned && pieces <= 8 * 1024 && pieces >= 1) launch_quantize_rows<DT, 1024>(rows, n, x, ldx, q, ldq, scales, s);
   else if (n <= 1024) hipLaunchKernelGGL((quantize_any_kernel<DT, 256>), dim3((unsigned)rows), dim3(256), 0, s, x, ldx, q, ldq, scales, n);
   else hipLaunchKernelGGL((quantize_any_kernel<DT, 1024>), dim3((unsigned)rows), dim3(1024), 0, s, x, ldx, q, ldq, scales, n);

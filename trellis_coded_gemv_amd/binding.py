@@ -126,9 +126,15 @@ def _check(status: int, where: str) -> None:
         raise TgError(status, where)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -409,10 +415,11 @@ _DTYPES = {}
 
 
 def _dtype_code(dtype, where: str) -> int:
-    if not _DTYPES:
+    code = _DTYPES.get(dtype)
+    if code is None:
         torch = _torch()
         _DTYPES.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
-    code = _DTYPES.get(dtype)
+        code = _DTYPES.get(dtype)
     if code is None:
         raise ValueError(f"{where}: expected float32, float16 or bfloat16, got {dtype}")
     return code
@@ -423,20 +430,15 @@ def _expect(ok: bool, where: str, what: str) -> None:
         raise ValueError(f"{where}: {what}")
 
 
-def _common_device(where: str, *tensors) -> int:
-    """Index of the GPU that holds every tensor (None among them is skipped)."""
-    at = tensors[0].get_device()
+def _common_device(where: str, first, *others) -> int:
+    """Index of the GPU that holds every tensor (None among the others is skipped)."""
+    at = first.get_device()
     if at < 0:
-        raise ValueError(f"{where}: expected tensors on a GPU, got {tensors[0].device}")
-    for t in tensors:
+        raise ValueError(f"{where}: expected tensors on a GPU, got {first.device}")
+    for t in others:
         if t is not None and t.get_device() != at:
-            raise ValueError(f"{where}: tensors on {tensors[0].device} and {t.device}")
+            raise ValueError(f"{where}: tensors on {first.device} and {t.device}")
     return at
-
-
-def _elsewhere(torch, at: int, stream) -> bool:
-    """Whether a call has to enter another device or stream than the current ones."""
-    return stream is not None or at != torch._C._cuda_getDevice()
 
 
 class _Entered:
@@ -459,10 +461,6 @@ class _Entered:
             c.__exit__(*exc)
 
 
-def _current(torch, at: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(at)
-
-
 def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int = 1, topk_group: int = 1,
               group_top: int = 1, renormalize: bool = True, scale: float = 1.0, sel=None, weights=None, stream=None):
     """Expert ids int32 [tokens, top_k] and weights fp32 [tokens, top_k] of router logits [tokens, experts] (fp32, fp16 or
@@ -480,7 +478,7 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int
     if bias is not None:
         _expect(bias.dtype == torch.float32 and bias.shape == (experts,) and bias.is_contiguous(), w, f"expected a float32 bias [{experts}]")
     at = _common_device(w, logits, bias, sel, weights)
-    if _elsewhere(torch, at, stream):
+    if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
             return moe_route(logits, top_k, bias, sigmoid, n_group, topk_group, group_top, renormalize, scale, sel, weights)
     if sel is None:
@@ -493,8 +491,10 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int
         _expect(weights.dtype == torch.float32 and weights.shape == (tokens, top_k) and weights.is_contiguous(), w,
                 f"expected weights float32 [{tokens}, {top_k}]")
     flags = (TG_ROUTE_SIGMOID if sigmoid else 0) | (TG_ROUTE_RENORM if renormalize else 0)
-    _check(lib().moe_route(tokens, experts, top_k, logits.data_ptr(), dtype, ld if tokens > 1 else experts, None if bias is None else bias.data_ptr(),
-                           n_group, topk_group, group_top, flags, scale, sel.data_ptr(), weights.data_ptr(), _current(torch, at)), w)
+    status = (_lib or lib()).moe_route(tokens, experts, top_k, logits.data_ptr(), dtype, ld if tokens > 1 else experts, None if bias is None else bias.data_ptr(),
+                           n_group, topk_group, group_top, flags, scale, sel.data_ptr(), weights.data_ptr(), torch._C._cuda_getCurrentRawStream(at))
+    if status:
+        raise TgError(status, w)
     return sel, weights
 
 
@@ -507,7 +507,7 @@ def moe_group(sel, experts: int, offsets=None, order=None, stream=None):
         raise ValueError(f"{w}: expected contiguous int32 ids")
     pairs = sel.numel()
     at = _common_device(w, sel, offsets, order)
-    if _elsewhere(torch, at, stream):
+    if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
             return moe_group(sel, experts, offsets, order)
     if offsets is None:
@@ -519,7 +519,9 @@ def moe_group(sel, experts: int, offsets=None, order=None, stream=None):
         order = torch.empty(pairs, dtype=torch.int32, device=sel.device)
     else:
         _expect(order.dtype == torch.int32 and order.shape == (pairs,) and order.is_contiguous(), w, f"expected order int32 [{pairs}]")
-    _check(lib().moe_group(pairs, experts, sel.data_ptr(), offsets.data_ptr(), order.data_ptr(), _current(torch, at)), w)
+    status = (_lib or lib()).moe_group(pairs, experts, sel.data_ptr(), offsets.data_ptr(), order.data_ptr(), torch._C._cuda_getCurrentRawStream(at))
+    if status:
+        raise TgError(status, w)
     return offsets, order
 
 
@@ -532,29 +534,35 @@ def int8_quantize(x, q=None, scales=None, stream=None):
     if len(shape) < 1 or x.numel() == 0:
         raise ValueError(f"{w}: expected rows [..., n]")
     at = _common_device(w, x, q, scales)
-    if _elsewhere(torch, at, stream):
+    if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
             return int8_quantize(x, q, scales)
     lead, n = shape[:-1], shape[-1]
     x2 = x if len(shape) == 2 else x.reshape(-1, n)
+    rows, ldq = x2.shape[0], n
     ldx, inner = x2.stride()
     if inner != 1 and n > 1:
         x2 = x2.contiguous()
         ldx = n
-    rows, ldq = x2.shape[0], n
     if q is None:
-        q = torch.empty(*shape, dtype=torch.int8, device=x.device)
+        q = torch.empty(rows, n, dtype=torch.int8, device=x.device)
+        if x2 is not x:
+            q = q.view(shape)
     else:
         _expect(q.dtype == torch.int8 and q.shape == shape and (q.is_contiguous() or (q.dim() == 2 and q.stride(1) == 1 and q.stride(0) >= n)),
                 w, "expected q int8 in the shape of x, with neighbouring values")
         if q.dim() == 2 and rows > 1:
             ldq = q.stride(0)
     if scales is None:
-        scales = torch.empty(lead, dtype=torch.float32, device=x.device)
+        scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+        if x2 is not x:
+            scales = scales.view(lead)
     else:
         _expect(scales.dtype == torch.float32 and scales.shape == lead and scales.is_contiguous(), w, "expected a float32 scale for each row")
-    _check(lib().int8_quantize(rows, n, x2.data_ptr(), dtype, ldx if rows > 1 else n, q.data_ptr(), ldq, scales.data_ptr(),
-                               _current(torch, at)), w)
+    status = (_lib or lib()).int8_quantize(rows, n, x2.data_ptr(), dtype, ldx if rows > 1 else n, q.data_ptr(), ldq, scales.data_ptr(),
+                               torch._C._cuda_getCurrentRawStream(at))
+    if status:
+        raise TgError(status, w)
     return q, scales
 
 
@@ -635,14 +643,16 @@ def int8_gemm(layer: "Int8Layer", xq, xs, Y=None, out_dtype=None, ws=None, strea
     m, n = layer.m, layer.n
     M, ldx = _int8_rows(torch, w, n, xq, xs)
     at = _common_device(w, xq, xs, layer.q, Y, ws)
-    if _elsewhere(torch, at, stream):
+    if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
             return int8_gemm(layer, xq, xs, Y, out_dtype, ws)
     Y, code, ldy = _int8_out(torch, w, Y, M, m, out_dtype, xq)
     if ws is None:
         ws = int8_workspace(layer, M)
-    _check(lib().int8_gemm(M, m, n, xq.data_ptr(), ldx, xs.data_ptr(), layer.q.data_ptr(), layer.ldw, layer.scales.data_ptr(),
-                           Y.data_ptr(), code, ldy, ws.data_ptr(), ws.numel() * ws.element_size(), _current(torch, at)), w)
+    status = (_lib or lib()).int8_gemm(M, m, n, xq.data_ptr(), ldx, xs.data_ptr(), layer.q.data_ptr(), layer.ldw, layer.scales.data_ptr(),
+                           Y.data_ptr(), code, ldy, ws.data_ptr(), ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(at))
+    if status:
+        raise TgError(status, w)
     return Y
 
 
@@ -659,13 +669,15 @@ def int8_gemm_grouped(experts: "Int8Experts", xq, xs, offsets, order, pairs_per_
     if offsets.dtype != torch.int32 or offsets.shape != (count + 1,) or not offsets.is_contiguous():
         raise ValueError(f"{w}: expected offsets int32 [{count + 1}]")
     at = _common_device(w, xq, xs, experts.q, offsets, order, Y)
-    if _elsewhere(torch, at, stream):
+    if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
             return int8_gemm_grouped(experts, xq, xs, offsets, order, pairs_per_row, Y, out_dtype)
     Y, code, ldy = _int8_out(torch, w, Y, pairs, m, out_dtype, xq)
-    _check(lib().int8_gemm_grouped(pairs, count, m, n, xq.data_ptr(), ldx, xs.data_ptr(), int(pairs_per_row), experts.q.data_ptr(),
+    status = (_lib or lib()).int8_gemm_grouped(pairs, count, m, n, xq.data_ptr(), ldx, xs.data_ptr(), int(pairs_per_row), experts.q.data_ptr(),
                                    experts.scales.data_ptr(), offsets.data_ptr(), order.data_ptr(), Y.data_ptr(), code, ldy,
-                                   _current(torch, at)), w)
+                                   torch._C._cuda_getCurrentRawStream(at))
+    if status:
+        raise TgError(status, w)
     return Y
 
 
@@ -684,7 +696,7 @@ class Int8Linear:
     def forward(self, x, stream=None):
         n, m = self.layer.n, self.layer.m
         _expect(x.shape[-1] == n, "Int8Linear", f"expected activations [..., {n}], got {tuple(x.shape)}")
-        if _elsewhere(_torch(), _common_device("Int8Linear", x, self.layer.q), stream):
+        if stream is not None or _common_device("Int8Linear", x, self.layer.q) != _torch()._C._cuda_getDevice():
             with _Entered(x.get_device(), stream):
                 return self.forward(x)
         xq, xs = int8_quantize(x)

@@ -23,7 +23,8 @@ def _near(y, ref, dtype):
 
 
 @pytest.mark.parametrize("rows,n,pad", [(1, 1, 0), (3, 7, 0), (1, 16, 0), (5, 64, 1), (4, 100, 8), (2, 255, 0), (2, 257, 3), (3, 2048, 0),
-                                        (2, 8192, 16), (1, 8192, 0), (300, 130, 0), (2, 14336, 0), (1, 14337, 0), (1, 40000, 0), (2, 70001, 5)])
+                                        (2, 8192, 16), (1, 8192, 0), (300, 130, 0), (2, 14336, 0), (1, 14337, 0), (1, 40000, 0), (2, 70001, 5),
+                                        (600, 4104, 0), (66000, 8, 0), (65537, 3, 1)])
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
 def test_quantize_is_exact(rows, n, pad, dtype):
     dev = device()
@@ -40,11 +41,13 @@ def test_quantize_is_exact(rows, n, pad, dtype):
     scales = torch.full((rows + 2,), 99.0, device=dev)
     tg.int8_quantize(xv, q=q[:, :n], scales=scales[1:-1])
     torch.cuda.synchronize()
-    qr, sr = oracle.quantize(x[:, :n].double().numpy())
+    # the oracle works on fractions: of many rows, it takes the ends and some between
+    pick = np.arange(rows) if rows <= 300 else np.unique(np.r_[0, rows - 1, 65534, 65535, 65536, rng.integers(0, rows, 8)].clip(0, rows - 1))
+    qr, sr = oracle.quantize(x[pick, :n].double().numpy())
     got = q.cpu().numpy()
-    assert np.array_equal(got[:, :n], qr) and (got[:, n:] == 99).all()
+    assert np.array_equal(got[pick, :n], qr) and (got[:, n:] == 99).all()
     s = scales.double().cpu().numpy()
-    assert s[0] == s[-1] == 99 and np.all(np.abs(s[1:-1] - sr) <= STEP * sr)
+    assert s[0] == s[-1] == 99 and np.all(np.abs(s[1:-1][pick] - sr) <= STEP * sr)
 
 
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])

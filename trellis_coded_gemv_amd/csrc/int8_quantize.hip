@@ -58,10 +58,11 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top, float* scale) {
 template <int DT, int THREADS, int PER>
 __global__ __launch_bounds__(THREADS) void quantize_rows_kernel(const void* __restrict__ x, int64_t ldx,
                                                                 int8_t* __restrict__ q, int64_t ldq,
-                                                                float* __restrict__ scales, int n) {
+                                                                float* __restrict__ scales, int n, int rows) {
   constexpr int VEC = DT == kF32 ? 4 : 8;
   __shared__ uint32_t wmax[THREADS / 64];
-  const int row = blockIdx.x;
+  const int row = blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= rows) return;
   const int64_t base = (int64_t)row * ldx;
   const int pieces = n / VEC, rest = n - pieces * VEC;
   u32x4 v[PER];
@@ -126,9 +127,10 @@ __global__ __launch_bounds__(THREADS) void quantize_rows_kernel(const void* __re
 template <int DT, int THREADS>
 __global__ __launch_bounds__(THREADS) void quantize_any_kernel(const void* __restrict__ x, int64_t ldx,
                                                                int8_t* __restrict__ q, int64_t ldq,
-                                                               float* __restrict__ scales, int n) {
+                                                               float* __restrict__ scales, int n, int rows) {
   __shared__ uint32_t wmax[THREADS / 64];
-  const int row = blockIdx.x;
+  const int row = blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= rows) return;
   const int64_t base = (int64_t)row * ldx;
   uint32_t top = 0;
 #pragma unroll 4
@@ -141,6 +143,12 @@ __global__ __launch_bounds__(THREADS) void quantize_any_kernel(const void* __res
     qr[i] = r.finite ? (int8_t)quantize_step(load_elem<DT>(x, base + i), r.inv) : (int8_t)0;
 }
 
+// A workgroup for each row; one dimension of a launch holds fewer than 2^32 threads.
+static dim3 row_grid(int rows) {
+  const unsigned x = rows < 65536 ? (unsigned)rows : 65536u;
+  return dim3(x, ((unsigned)rows + x - 1) / x);
+}
+
 // A row is a workgroup's, of 256 threads where a thread then holds one 16-byte piece (4096 rows of 1024 fp16 values: 5.6
 // us, with 1024 threads 14.2), or up to four of many rows (2048 x 8192: 11.6 and 13.1), else of 1024 (1 x 8192: 2.7 and
 // 3.1; 4096 x 14336: 30 and 48).
@@ -149,11 +157,11 @@ static void launch_quantize_rows(int rows, int n, const void* x, int64_t ldx, in
                                  hipStream_t s) {
   constexpr int VEC = DT == kF32 ? 4 : 8;
   const int per = (n / VEC + THREADS - 1) / THREADS;
-  const dim3 grid((unsigned)rows), block(THREADS);
-  if (per <= 1) hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 1>), grid, block, 0, s, x, ldx, q, ldq, scales, n);
-  else if (per <= 2) hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 2>), grid, block, 0, s, x, ldx, q, ldq, scales, n);
-  else if (per <= 4) hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 4>), grid, block, 0, s, x, ldx, q, ldq, scales, n);
-  else hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 8>), grid, block, 0, s, x, ldx, q, ldq, scales, n);
+  const dim3 grid = row_grid(rows), block(THREADS);
+  if (per <= 1) hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 1>), grid, block, 0, s, x, ldx, q, ldq, scales, n, rows);
+  else if (per <= 2) hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 2>), grid, block, 0, s, x, ldx, q, ldq, scales, n, rows);
+  else if (per <= 4) hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 4>), grid, block, 0, s, x, ldx, q, ldq, scales, n, rows);
+  else hipLaunchKernelGGL((quantize_rows_kernel<DT, THREADS, 8>), grid, block, 0, s, x, ldx, q, ldq, scales, n, rows);
 }
 
 template <int DT>
@@ -166,8 +174,8 @@ static hipError_t launch_quantize_t(int rows, int n, const void* x, int64_t ldx,
   if (aligned && pieces <= 256 && pieces >= 1) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
   else if (aligned && pieces <= 4 * 256 && rows >= 512) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
   else if (aligned && pieces <= 8 * 1024 && pieces >= 1) launch_quantize_rows<DT, 1024>(rows, n, x, ldx, q, ldq, scales, s);
-  else if (n <= 1024) hipLaunchKernelGGL((quantize_any_kernel<DT, 256>), dim3((unsigned)rows), dim3(256), 0, s, x, ldx, q, ldq, scales, n);
-  else hipLaunchKernelGGL((quantize_any_kernel<DT, 1024>), dim3((unsigned)rows), dim3(1024), 0, s, x, ldx, q, ldq, scales, n);
+  else if (n <= 1024) hipLaunchKernelGGL((quantize_any_kernel<DT, 256>), row_grid(rows), dim3(256), 0, s, x, ldx, q, ldq, scales, n, rows);
+  else hipLaunchKernelGGL((quantize_any_kernel<DT, 1024>), row_grid(rows), dim3(1024), 0, s, x, ldx, q, ldq, scales, n, rows);
   return hipGetLastError();
 }
 

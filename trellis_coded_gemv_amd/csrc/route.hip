@@ -194,7 +194,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
   };
   const int inverse = ((1 << 20) + size - 1) / size;        // e / size = e * inverse >> 20 for e < 2^10, size <= 2^10
   const bool one_group = V == 1 || size % V == 0;           // a lane's experts lie in one group
-  auto in_kept = [&](uint64_t kept, int i) { return (kept >> (((lane * V + (one_group ? 0 : i)) * inverse) >> 20)) & 1; };
+  auto in_kept = [&](uint64_t kept, int i) { return (kept >> ((((lane * V + (one_group ? 0 : i)) * inverse) >> 20) & 63)) & 1; };
 
   int my_id = -1, found = 0;   // lane i keeps the i-th expert found
   bool sure = true, fuzzy = false;

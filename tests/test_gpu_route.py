@@ -66,6 +66,30 @@ def test_route_matches_oracle(tokens, experts, top_k, dtype, opts):
     _check(torch, dev, l, top_k, opts, pad=tokens % 3, dtype=dtype)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("experts", [40, 128, 192, 256, 384, 512, 1008, 1024])
+@pytest.mark.parametrize("shift,pad", [(0, 0), (0, 16), (1, 15), (0, 1), (8, 0)])
+def test_rows_read_at_once_or_one_by_one(dtype, experts, shift, pad):
+    """Rows at every alignment, aligned and shifted biases; what lies beside the rows is never used."""
+    dev = device()
+    import torch
+    say("route rows", dtype, experts, shift, pad)
+    rng = np.random.default_rng(experts + shift * 7 + pad)
+    T, top_k, ld = 5, 6, experts + pad
+    l = torch.from_numpy((rng.normal(size=(T, experts)) * 2).astype(np.float32)).to(getattr(torch, dtype))
+    flat = torch.full((shift + T * ld,), float("nan"), dtype=l.dtype, device=dev)
+    view = flat[shift:].as_strided((T, experts), (ld, 1))
+    view.copy_(l)
+    bias = rng.normal(size=experts).astype(np.float32) * 0.1
+    wide_bias = torch.full((shift + experts,), float("nan"), device=dev)
+    wide_bias[shift:].copy_(torch.from_numpy(bias))
+    for b, b_np in [(None, None), (wide_bias[shift:], bias)]:
+        sel, w = tg.moe_route(view, top_k, bias=b, sigmoid=True)
+        ids, ref = oracle.route(l.float().numpy(), top_k, bias=b_np, sigmoid=True)
+        assert np.array_equal(sel.cpu().numpy(), ids)
+        assert np.all(np.abs(w.cpu().numpy().astype(np.float64) - ref) <= W_TOL * ref)
+
+
 @pytest.mark.parametrize("opts", [{}, dict(sigmoid=True), dict(n_group=8, topk_group=3, group_top=2), dict(sigmoid=True, zero_bias=True)])
 def test_equal_logits_go_to_the_lowest_index(opts):
     dev = device()

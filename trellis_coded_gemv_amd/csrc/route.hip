@@ -38,6 +38,37 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
 }
 
+template <int DT>
+__device__ __forceinline__ float logit(const void* p, int64_t i) {
+  if constexpr (DT == kF32) return reinterpret_cast<const float*>(p)[i];
+  const uint16_t b = reinterpret_cast<const uint16_t*>(p)[i];
+  if constexpr (DT == kF16) return half_bits_to_float(b);
+  return __builtin_bit_cast(float, (uint32_t)b << 16);
+}
+
+// V neighbouring values at a multiple of their size, up to 16 bytes at once.
+template <int V, int DT>
+__device__ __forceinline__ void load_neighbours(const void* p, int64_t at, float (&f)[V]) {
+  constexpr int kBytes = V * (DT == kF32 ? 4 : 2), kWords = kBytes >= 16 ? 4 : kBytes / 4;
+  if constexpr (kWords == 0) {
+    f[0] = logit<DT>(p, at);
+  } else {
+    typedef uint32_t words __attribute__((ext_vector_type(kWords)));
+    constexpr int kEach = kWords * (DT == kF32 ? 1 : 2);    // values of one load
+#pragma unroll
+    for (int d = 0; d < V / kEach; ++d) {
+      const words w = *reinterpret_cast<const words*>(reinterpret_cast<const char*>(p) + (at + d * kEach) * (DT == kF32 ? 4 : 2));
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const uint32_t word = w[DT == kF32 ? i : i / 2];
+        if constexpr (DT == kF32) f[d * kEach + i] = __builtin_bit_cast(float, word);
+        else if constexpr (DT == kF16) f[d * kEach + i] = half_bits_to_float((uint16_t)(word >> (16 * (i & 1))));
+        else f[d * kEach + i] = __builtin_bit_cast(float, i & 1 ? word & 0xFFFF0000u : word << 16);
+      }
+    }
+  }
+}
+
 // Numbers as words of the same order; none is 0.
 __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t b = __builtin_bit_cast(uint32_t, f + 0.0f);   // -0 and +0 are equal
@@ -88,14 +119,6 @@ __device__ __forceinline__ double wave_sum(double v) {
 __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
-}
-
-template <int DT>
-__device__ __forceinline__ float logit(const void* p, int64_t i) {
-  if constexpr (DT == kF32) return reinterpret_cast<const float*>(p)[i];
-  const uint16_t b = reinterpret_cast<const uint16_t*>(p)[i];
-  if constexpr (DT == kF16) return half_bits_to_float(b);
-  return __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
 __device__ __forceinline__ float lane_value(float v, int lane) {
@@ -151,11 +174,22 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
   const float inf = __builtin_huge_valf();
   float l[V], bias[V];
   const int64_t at0 = (int64_t)token * a.ld;
+  if (a.whole) {            // a lane's experts are all there, or none, and lie at a multiple of their size
+    const int e = min(lane * V, a.experts - V);
+    load_neighbours<V, DT>(a.logits, at0 + e, l);
+    if (a.bias) load_neighbours<V, kF32>(a.bias, e, bias);
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    l[i] = e < a.experts ? logit<DT>(a.logits, at0 + e) : -inf;
-    bias[i] = a.bias && e < a.experts ? a.bias[e] : 0.f;
+    for (int i = 0; i < V; ++i) {
+      l[i] = lane * V < a.experts ? l[i] : -inf;
+      bias[i] = a.bias && lane * V < a.experts ? bias[i] : 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = lane * V + i;
+      l[i] = e < a.experts ? logit<DT>(a.logits, at0 + e) : -inf;
+      bias[i] = a.bias && e < a.experts ? a.bias[e] : 0.f;
+    }
   }
   float most = -inf;
   bool poison = false;
@@ -245,23 +279,26 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
       return wave_max_u32(m);
     };
     auto round = [&](uint32_t top) {
-      uint64_t hit[V], any = 0;
+      bool hit[V], any = false;
+      int first = lane * V;                                 // this lane's first expert with that key
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        hit[i] = __ballot(key[i] == top);
+        hit[i] = key[i] == top;
         any |= hit[i];
       }
-      const int owner = __builtin_ctzll(any);
-      int at = 0;
 #pragma unroll
-      for (int i = V - 1; i > 0; --i) at = (hit[i] >> owner) & 1 ? i : at;
-      if ((hit[0] >> owner) & 1) at = 0;
-      const int id = owner * V + at;
+      for (int i = V - 1; i >= 0; --i) first = hit[i] ? lane * V + i : first;
+      const int owner = __builtin_ctzll(__ballot(any));
+      const int id = __builtin_amdgcn_readlane(first, owner);
       my_id = lane == found ? id : my_id;
       my_key = lane == found ? top : my_key;
       ++found;
+      bool open = lane == owner;
 #pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = lane == (i == at ? owner : -1) ? 0u : key[i];
+      for (int i = 0; i < V; ++i) {
+        key[i] = open && hit[i] ? 0u : key[i];
+        open = open && !hit[i];
+      }
     };
     uint32_t top = 0;
     while (sure && found < a.top_k) {
@@ -381,16 +418,22 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
 }
 
 // Bound by instruction issue and the rounds' chain of dependent steps: 8192 tokens x 256 experts in 8 groups, top 8, take
-// 14.5 us (603 vector and 558 scalar instructions a token; 8.4 MB, 1.7 us of them), one token of 128 experts 3.4 us. Four
+// 14.6 us (681 vector and 386 scalar instructions a token; 15.6 us with an expert read at a time; 8.9 MB, 1.7 us of them),
+// one token of 128 experts 3.4 us. Four
 // tokens share a workgroup where there are many; one each keeps a short batch spread over the card.
 template <int DT>
-static hipError_t launch_route_t(const RouteArgs& a, hipStream_t s) {
+static hipError_t launch_route_t(const RouteArgs& args, hipStream_t s) {
+  RouteArgs a = args;
   const int waves = a.tokens >= 1024 ? kRouteWaves : 1;
   const dim3 grid((unsigned)((a.tokens + waves - 1) / waves)), block(64 * waves);
-  if (a.experts <= 64) hipLaunchKernelGGL((route_kernel<1, DT>), grid, block, 0, s, a);
-  else if (a.experts <= 128) hipLaunchKernelGGL((route_kernel<2, DT>), grid, block, 0, s, a);
-  else if (a.experts <= 256) hipLaunchKernelGGL((route_kernel<4, DT>), grid, block, 0, s, a);
-  else if (a.experts <= 512) hipLaunchKernelGGL((route_kernel<8, DT>), grid, block, 0, s, a);
+  const int v = a.experts <= 64 ? 1 : a.experts <= 128 ? 2 : a.experts <= 256 ? 4 : a.experts <= 512 ? 8 : 16;
+  const size_t each = DT == kF32 ? 4 : 2, bytes = v * each < 16 ? v * each : 16;
+  a.whole = a.experts % v == 0 && (uintptr_t)a.logits % bytes == 0 && (a.tokens == 1 || a.ld * each % bytes == 0) &&
+            (!a.bias || (uintptr_t)a.bias % (v * 4 < 16 ? v * 4 : 16) == 0);
+  if (v == 1) hipLaunchKernelGGL((route_kernel<1, DT>), grid, block, 0, s, a);
+  else if (v == 2) hipLaunchKernelGGL((route_kernel<2, DT>), grid, block, 0, s, a);
+  else if (v == 4) hipLaunchKernelGGL((route_kernel<4, DT>), grid, block, 0, s, a);
+  else if (v == 8) hipLaunchKernelGGL((route_kernel<8, DT>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((route_kernel<16, DT>), grid, block, 0, s, a);
   return hipGetLastError();
 }

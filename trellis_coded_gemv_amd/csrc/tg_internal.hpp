@@ -140,6 +140,7 @@ struct RouteArgs {
   int64_t ld;
   int32_t tokens, experts, top_k, n_group, topk_group, group_top;
   int32_t sigmoid, renorm;
+  int32_t whole;          // a lane's experts can be read at once (set by the launch)
   float scale;
 };
 hipError_t launch_moe_route(const RouteArgs& a, int dtype, hipStream_t s);

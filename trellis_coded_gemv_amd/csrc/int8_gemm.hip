@@ -5,12 +5,16 @@
 // work; an output is rounded three times in binary32 (the sum, and its product with either scale) and once more to a
 // 16-bit output type.
 //
-// What bounds it (MI355X, 2.2 GHz under this load): 4096 x 28672 x 8192 runs at 2530 TOP/s, 61% of what the matrix cores
-// reach on such values from registers alone (4035 TOP/s; 4900 on zeros: the card's power). With the loads to LDS alone the
-// same kernel takes 729 of 850 us, with the reads from LDS alone 323 us, so the way from L2 is next to the power what
-// holds it; 256 x 256 tiles ask least of it. The library's own 8-bit product takes 844 us there. 1 x 28672 x 8192 reads
-// 235 MB in 42 us (5.6 TB/s; a large copy moves 5.1). 8192 tokens over 128 experts, 1536 x 2048, top 8: 298 us, of which
-// the products of the partly filled tiles take about 225, first loads and lookups 42, the stores 35.
+// What bounds it (MI355X, 2.2 GHz under this load): 4096 x 28672 x 8192 runs at 2440-2530 TOP/s, 61% of what the matrix
+// cores reach on such values from registers alone (4035 TOP/s; 4900 on zeros: the card's power). The loads to LDS alone
+// take 508 of 789 us with these 256 x 256 tiles, and 722 of 899 with 256 x 128 (373 and 456 where every tile reads the
+// same rows, out of L2); the reads from LDS alone 323. So the way into LDS comes next to the power, and the largest tiles
+// ask least of it. The library's own 8-bit product takes 844 us there. 1 x 28672 x 8192 reads 235 MB in 42 us (5.6 TB/s; a
+// large copy moves 5.1). 8192 tokens over 128 experts, 1536 x 2048, top 8: 298 us, 220 of them the loads to LDS (187 if
+// the weights of 8 experts serve all), 35 the stores, 42 the first loads and lookups of the 4.5 row tiles of an expert.
+// Leaving out the products of rows that are not there changes nothing (295), workgroups that go on to a next tile and
+// begin its loads before the stores of the last lose (312 -> 320 with 256 x 128 tiles: loads wait for the stores before
+// them).
 //
 // v_mfma_i32_16x16x64_i8 with the layer's rows as its A operand and the activation rows as its B operand: lane l
 // supplies row l % 16 and the 16 bytes at 16 (l / 16) of 64 bytes of the inner axis on both sides, and ends with four

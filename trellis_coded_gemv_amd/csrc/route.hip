@@ -419,8 +419,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
 
 // Bound by instruction issue and the rounds' chain of dependent steps: 8192 tokens x 256 experts in 8 groups, top 8, take
 // 14.6 us (681 vector and 386 scalar instructions a token; 15.6 us with an expert read at a time; 8.9 MB, 1.7 us of them),
-// one token of 128 experts 3.4 us. Four
-// tokens share a workgroup where there are many; one each keeps a short batch spread over the card.
+// one token of 128 experts 3.4 us. Four tokens share a workgroup where there are many; one each keeps a short batch
+// spread over the card.
 template <int DT>
 static hipError_t launch_route_t(const RouteArgs& args, hipStream_t s) {
   RouteArgs a = args;

@@ -468,8 +468,8 @@ size_t tg_encode_workspace_size(int32_t n_tiles, int32_t k_bits, int32_t code_id
  *     w   = scale * s[ids], with TG_ROUTE_RENORM scale * s[ids] / sum(s[ids]).
  * With n_group > 1 the experts form n_group equal neighbouring groups; a group's value is the largest
  * r in it (group_top 1) or the sum of its two largest (group_top 2), and only experts of the topk_group
- * groups of largest value are selected (equal ones by their index). Scores, values and comparisons are
- * formed in binary64; a weight is rounded to binary32 once.
+ * groups of largest value are selected (equal ones by their index). The ids are those of scores, values
+ * and comparisons in binary64; a weight is formed there and rounded to binary32 once.
  * An expert whose logit or bias is -infinity is not available: it is never selected, and a group value
  * sums over the available ones (a group without any is not selected). Slots left over when fewer than
  * top_k experts are available get id -1 and weight 0, which trellis_moe_block, trellis_gemv_grouped and

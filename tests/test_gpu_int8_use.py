@@ -75,6 +75,40 @@ def test_two_graphs_share_a_workspace_on_one_stream():
         assert torch.equal(ya, ra) and torch.equal(yb, rb)
 
 
+def test_first_linear_call_under_capture():
+    """The workspace of a layer first used (or first used with so many rows) inside a capture is the graph's: eager calls before
+    the first replay and between replays have their own."""
+    dev = device()
+    import torch
+    say("int8 linear first called under capture")
+    L = _layer(torch, dev, 4096, 14336, 21)
+    xs = [torch.randn(r, 14336, generator=torch.Generator().manual_seed(22 + r)).half().to(dev) for r in (61, 128)]
+    refs = [tg.Int8Linear(L)(x).clone() for x in xs]
+    lin, outs = tg.Int8Linear(L), [torch.empty_like(r) for r in refs]
+    graphs = []
+    for x, out, ref in zip(xs, outs, refs):
+        graphs.append(_capture(torch, lambda: out.copy_(lin(x))))
+        assert torch.equal(lin(x), ref)                              # before its graph has run
+    for _ in range(3):
+        for x, out, ref, g in zip(xs, outs, refs, graphs):
+            out.fill_(float("nan"))
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, ref) and torch.equal(lin(x), ref)
+
+
+def test_workspace_refused():
+    dev = device()
+    import torch
+    L = _layer(torch, dev, 64, 2048, 30)
+    xq, xs = _rows(torch, dev, 4, 2048, 31)
+    need = tg.int8_workspace(L, 4).numel()
+    with pytest.raises(ValueError, match="contiguous"):
+        tg.int8_gemm(L, xq, xs, ws=torch.zeros(1, dtype=torch.uint8, device=dev).expand(2 * need))
+    with pytest.raises(tg.TgError):
+        tg.int8_gemm(L, xq, xs, ws=torch.zeros(need - 256, dtype=torch.uint8, device=dev))
+
+
 def _block(torch, x, router, gu, dn, top_k, out):
     """Router, groups, both expert products and the combine of a block over many tokens."""
     tokens, hidden = x.shape

@@ -649,6 +649,8 @@ def int8_gemm(layer: "Int8Layer", xq, xs, Y=None, out_dtype=None, ws=None, strea
     Y, code, ldy = _int8_out(torch, w, Y, M, m, out_dtype, xq)
     if ws is None:
         ws = int8_workspace(layer, M)
+    elif not ws.is_contiguous():
+        raise ValueError(f"{w}: expected a contiguous workspace")
     status = (_lib or lib()).int8_gemm(M, m, n, xq.data_ptr(), ldx, xs.data_ptr(), layer.q.data_ptr(), layer.ldw, layer.scales.data_ptr(),
                            Y.data_ptr(), code, ldy, ws.data_ptr(), ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(at))
     if status:
@@ -686,7 +688,8 @@ class Int8Linear:
 
     `forward(x)` takes fp32, fp16 or bf16 activations [..., n] on the device, quantises each row with a scale of its own
     (int8_quantize) and returns fp32 [..., m] (int8_gemm). The workspace is kept and replaced by a larger one when a row
-    count needs it (the earlier ones live on, for graphs that were captured with them); calls are ordered on one stream.
+    count needs it (the earlier ones live on, for graphs that were captured with them; a call under capture that needs a
+    larger one takes the graph's own, cleared at each replay); calls are ordered on one stream.
     """
 
     def __init__(self, layer: "Int8Layer"):
@@ -695,16 +698,19 @@ class Int8Linear:
 
     def forward(self, x, stream=None):
         n, m = self.layer.n, self.layer.m
-        _expect(x.shape[-1] == n, "Int8Linear", f"expected activations [..., {n}], got {tuple(x.shape)}")
+        _expect(x.dim() > 0 and x.shape[-1] == n, "Int8Linear", f"expected activations [..., {n}], got {tuple(x.shape)}")
         if stream is not None or _common_device("Int8Linear", x, self.layer.q) != _torch()._C._cuda_getDevice():
             with _Entered(x.get_device(), stream):
                 return self.forward(x)
         xq, xs = int8_quantize(x)
         xq, xs = xq.view(-1, n), xs.view(-1)
-        if self._ws is None or self._ws.numel() < lib().tg_int8_workspace_size(xq.shape[0], m, n):
-            self._earlier.append(self._ws)
-            self._ws = int8_workspace(self.layer, xq.shape[0])
-        return int8_gemm(self.layer, xq, xs, ws=self._ws).reshape(x.shape[:-1] + (m,))
+        ws = self._ws
+        if ws is None or ws.numel() < lib().tg_int8_workspace_size(xq.shape[0], m, n):
+            ws = int8_workspace(self.layer, xq.shape[0])
+            if not _torch().cuda.is_current_stream_capturing():   # else its zeros are the graph's, there at its replays alone
+                self._earlier.append(self._ws)
+                self._ws = ws
+        return int8_gemm(self.layer, xq, xs, ws=ws).reshape(x.shape[:-1] + (m,))
 
     __call__ = forward
 

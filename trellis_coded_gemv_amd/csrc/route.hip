@@ -1,8 +1,8 @@
 // Routing of tokens to experts: scores, groups, the top_k ids with their weights (moe_route), and the routed pairs in
 // expert order (moe_group).
 //
-// An id is decided by comparing scores, so scores, keys and group values are formed in binary64 and equal ones go to
-// the lowest index; a weight is rounded to binary32 once.
+// An id is decided by comparing scores: the ids are those of binary64 scores, keys and group values, equal ones in
+// the order of the experts; a weight is formed in binary64 and rounded to binary32 once.
 #include "tg_device.hpp"
 #include "tg_internal.hpp"
 

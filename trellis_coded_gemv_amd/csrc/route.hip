@@ -3,6 +3,8 @@
 //
 // An id is decided by comparing scores: the ids are those of binary64 scores, keys and group values, equal ones in
 // the order of the experts; a weight is formed in binary64 and rounded to binary32 once.
+#include <type_traits>
+
 #include "tg_device.hpp"
 #include "tg_internal.hpp"
 
@@ -455,6 +457,12 @@ hipError_t launch_moe_route(const RouteArgs& a, int dtype, hipStream_t s) {
 // ---------------------------------------------------------------------------
 constexpr int kGroupSteps = 32;   // steps of 256 ids whose hits a wave keeps: 16 * 32 * 256 = 2^17 pairs
 
+// 2 v + this lane's bit of the mask, in one addition with carry.
+__device__ __forceinline__ uint32_t twice_plus(uint32_t v, uint64_t mask) {
+  asm("v_addc_co_u32_e64 %0, vcc, %0, %0, %1" : "+v"(v) : "s"(mask) : "vcc");
+  return v;
+}
+
 template <bool KEEP>
 __global__ __launch_bounds__(1024) void group_kernel(const int32_t* __restrict__ sel, int pairs, int experts, int wide,
                                                      int32_t* __restrict__ offsets, int32_t* __restrict__ order) {
@@ -493,13 +501,20 @@ __global__ __launch_bounds__(1024) void group_kernel(const int32_t* __restrict__
         u32x4 v[8];                                             // eight loads in flight
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4*>(sel + begin + (8 * b + i) * 256);
+        // A hit is doubled into its place by the addition that adds it: the first of 32 ends on top.
+        uint32_t hits = 0;
+        auto look = [&](auto last) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t id[4];
+          for (int i = 0; i < 8; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) id[c] = min(v[i][c], (uint32_t)experts);
-          kept[b] |= count(id) << (4 * i);
-        }
+            for (int c = 0; c < 4; ++c) {
+              less += __popcll(__ballot(v[i][c] < mine));
+              hits = twice_plus(hits, __ballot(decltype(last)::value ? v[i][c] >= mine : v[i][c] == mine));
+            }
+        };
+        if (mine == (uint32_t)experts) look(std::true_type{});
+        else look(std::false_type{});
+        kept[b] = __brev(hits);
       } else {
         for (int i = 0; i < 8 && 8 * b + i < steps; ++i) {
           uint32_t id[4];

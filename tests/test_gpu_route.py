@@ -178,6 +178,25 @@ def test_group_matches_oracle(tokens, experts, top_k):
     assert o[0] == o[-1] == r[0] == r[-1] == 77
 
 
+@pytest.mark.parametrize("pairs,experts,taken", [(1 << 17, 256, 255), (1 << 17, 256, 0), (1 << 17, 512, -1), (1 << 17, 3, 2),
+                                                 ((1 << 17) + 1, 256, 17), ((1 << 17) - 1, 256, -1), (700001, 256, 255), (700001, 40, 40)])
+def test_long_runs_of_one_id(pairs, experts, taken):
+    """Whole stretches of one id (an expert's, or none's) between random ones: every bit of a lane's batch is a hit."""
+    dev = device()
+    import torch
+    say("group runs", pairs, experts, taken)
+    rng = np.random.default_rng(pairs + experts)
+    sel = rng.integers(0, experts, size=(pairs, 1)).astype(np.int32)
+    sel[1000:pairs // 2] = taken
+    sel[pairs // 2 + 77:pairs - 5] = taken
+    for shift in (0, 1):                                             # aligned ids, and ids read one by one
+        t = torch.empty(pairs + shift, dtype=torch.int32, device=dev)[shift:]
+        t.copy_(torch.from_numpy(sel[:, 0]))
+        offsets, order = tg.moe_group(t, experts)
+        off, ordr = oracle.group(sel, experts)
+        assert np.array_equal(offsets.cpu().numpy(), off) and np.array_equal(order.cpu().numpy(), ordr)
+
+
 def test_one_expert_takes_all():
     dev = device()
     import torch

@@ -476,7 +476,6 @@ constexpr TileCost kTiles[] = {
     {32, 16, 2, 0.042f, 0.132f, 0.64f},   // TileShape<1, 1, 2, 1, 512, 3>
 };
 constexpr float kStreamRate = 5.3e6f;   // bytes per microsecond of a product that waits for memory alone
-constexpr int kComputeUnits = 256;
 
 // The cheapest shape and split of the inner axis: rounds of workgroups over the compute units, and the time that the
 // bytes take, of which a part is not hidden behind the other. Over the sweep this loses 0.4% against trying everything

@@ -447,15 +447,16 @@ hipError_t launch_moe_route(const RouteArgs& a, int dtype, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Bound by instruction issue: every workgroup looks at every id, 131072 pairs of 256 experts take 17 us, 512 pairs 3.8 us.
-// A single pass with a table of counts between workgroups would need a workspace and a second launch.
+// Pairs in expert order, stable, in one launch without a workspace: workgroup e reads all ids, counts those before its
+// own and writes its own pairs behind them. Its 16 waves take neighbouring stretches, a lane four neighbouring ids at a
+// time, so the order of the pairs is the order of waves, steps, lanes and ids.
 //
-// Pairs in expert order, stable, in one launch without a workspace: workgroup e (e == experts: the pairs without an
-// expert) reads all ids, counts those before its own and writes its own pairs behind them. Its 16 waves take
-// neighbouring stretches, a lane four neighbouring ids at a time, so the order of the pairs is the order of waves,
-// steps, lanes and ids.
+// Every workgroup looks at every id, with three vector instructions and two scalar ones, and that bounds it: 131072 pairs
+// of 256 experts take 10.0 us back to back (6 of them to read and count; 14.4 with the steps' hits placed one after
+// another), 512 pairs of 128 experts 2.8 us, 2^20 pairs 80 us. A table of counts between workgroups would let each look at
+// a part, for a workspace and a second launch.
 // ---------------------------------------------------------------------------
-constexpr int kGroupSteps = 32;   // steps of 256 ids whose hits a wave keeps: 16 * 32 * 256 = 2^17 pairs
+constexpr int kGroupBatches = 4;  // batches of 8 * 256 ids whose hits a wave keeps: 16 * 4 * 2048 = 2^17 pairs
 
 // 2 v + this lane's bit of the mask, in one addition with carry.
 __device__ __forceinline__ uint32_t twice_plus(uint32_t v, uint64_t mask) {
@@ -463,73 +464,58 @@ __device__ __forceinline__ uint32_t twice_plus(uint32_t v, uint64_t mask) {
   return v;
 }
 
-template <bool KEEP>
-__global__ __launch_bounds__(1024) void group_kernel(const int32_t* __restrict__ sel, int pairs, int experts, int wide,
-                                                     int32_t* __restrict__ offsets, int32_t* __restrict__ order) {
-  __shared__ int less_sh[16], same_sh[16];
+// The pairs of expert `mine` (NONE: mine == experts, those without one) -> their places, and where they end. KEEP: a
+// wave's batches fit kGroupBatches; else they are looked at again for the writing.
+template <bool KEEP, bool NONE>
+__device__ __forceinline__ int group_pairs(const int32_t* __restrict__ sel, int pairs, int experts, int wide, uint32_t mine,
+                                           int (&less_sh)[16], int (&same_sh)[16], int32_t* __restrict__ offsets,
+                                           int32_t* __restrict__ order) {
   const int lane = threadIdx.x & 63, wave = wave_id();
-  const uint32_t mine = blockIdx.x;
-  const int steps = (pairs + 4095) >> 12;                       // of 256 ids, per wave
-  const int begin = wave * steps * 256 + lane * 4;
-  auto load = [&](int step, uint32_t(&id)[4]) {                 // ids past the end: beyond every expert
-    const int p = begin + step * 256;
-    if (wide && p + 4 <= pairs) {
-      const u32x4 v = *reinterpret_cast<const u32x4*>(sel + p);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) id[c] = min(v[c], (uint32_t)experts);
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) id[c] = p + c < pairs ? min((uint32_t)sel[p + c], (uint32_t)experts) : 0xFFFFFFFFu;
-    }
-  };
-  uint32_t kept[kGroupSteps / 8] = {};                          // four bits per step: this lane's hits
-  int less = 0, same = 0;                                       // of the wave
-  auto count = [&](const uint32_t(&id)[4]) {
+  const int steps = (pairs + 4095) >> 12, batches = (steps + 7) >> 3;   // of 256 ids and of 8 steps, per wave
+  const int stretch = wave * steps * 256, begin = stretch + lane * 4;
+  // Batch b of this lane: a bit for each of its 32 ids that is the workgroup's; the wave's ids before it are added to less.
+  int less = 0;
+  auto look = [&](int b) {
     uint32_t hits = 0;
+    if (wide && 8 * b + 8 <= steps && stretch + (8 * b + 8) * 256 <= pairs) {
+      u32x4 v[8];                                             // eight loads in flight
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      less += __popcll(__ballot(id[c] < mine));
-      hits |= id[c] == mine ? 1u << c : 0u;
+      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4*>(sel + begin + (8 * b + i) * 256);
+      // A hit is doubled into its place by the addition that adds it: the first of 32 ends on top.
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          less += __popcll(__ballot(v[i][c] < mine));
+          hits = twice_plus(hits, __ballot(NONE ? v[i][c] >= mine : v[i][c] == mine));
+        }
+      return __brev(hits);
+    }
+    for (int i = 0; i < 8 && 8 * b + i < steps; ++i) {
+      const int p = begin + (8 * b + i) * 256;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool there = p + c < pairs;
+        const uint32_t id = there ? (uint32_t)sel[p + c] : 0u;
+        less += __popcll(__ballot(there && id < mine));
+        hits |= there && (NONE ? id >= mine : id == mine) ? 1u << (4 * i + c) : 0u;
+      }
     }
     return hits;
   };
+  uint32_t kept[kGroupBatches] = {};
+  int same = 0;
   if constexpr (KEEP) {
 #pragma unroll
-    for (int b = 0; b < kGroupSteps / 8; ++b) {
-      if (8 * b >= steps) break;
-      if (wide && 8 * b + 8 <= steps && wave * steps * 256 + (8 * b + 8) * 256 <= pairs) {
-        u32x4 v[8];                                             // eight loads in flight
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4*>(sel + begin + (8 * b + i) * 256);
-        // A hit is doubled into its place by the addition that adds it: the first of 32 ends on top.
-        uint32_t hits = 0;
-        auto look = [&](auto last) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              less += __popcll(__ballot(v[i][c] < mine));
-              hits = twice_plus(hits, __ballot(decltype(last)::value ? v[i][c] >= mine : v[i][c] == mine));
-            }
-        };
-        if (mine == (uint32_t)experts) look(std::true_type{});
-        else look(std::false_type{});
-        kept[b] = __brev(hits);
-      } else {
-        for (int i = 0; i < 8 && 8 * b + i < steps; ++i) {
-          uint32_t id[4];
-          load(8 * b + i, id);
-          kept[b] |= count(id) << (4 * i);
-        }
-      }
+    for (int b = 0; b < kGroupBatches; ++b) {
+      if (b >= batches) break;
+      int next = b;
+      asm volatile("" : "+s"(next) : "v"(less));              // one batch's loads at a time: four would not fit the registers
+      kept[b] = look(next);
       same += __popc(kept[b]);
     }
   } else {
-    for (int i = 0; i < steps; ++i) {
-      uint32_t id[4];
-      load(i, id);
-      same += __popc(count(id));
-    }
+    for (int b = 0; b < batches; ++b) same += __popc(look(b));
   }
   same = __builtin_amdgcn_readlane(wave_scan(same), 63);
   if (lane == 0) {
@@ -537,59 +523,74 @@ __global__ __launch_bounds__(1024) void group_kernel(const int32_t* __restrict__
     same_sh[wave] = same;
   }
   __syncthreads();
-  int base = 0, at = 0;
+  int at = 0, end = 0;
+#pragma unroll
   for (int w = 0; w < 16; ++w) {
-    base += less_sh[w];
-    if (w < wave) at += same_sh[w];
+    at += less_sh[w] + (w < wave ? same_sh[w] : 0);
+    end += less_sh[w] + same_sh[w];
   }
-  if (threadIdx.x == 0) offsets[mine] = base;                   // offsets[experts]: the pairs with an expert
-  if (same == 0) return;
-  at += base;
-  auto put = [&](int step, uint32_t hits, int to) {             // this lane's hits of a step
-    while (hits) {
-      order[to++] = begin + step * 256 + __builtin_ctz(hits);
-      hits &= hits - 1;
+  at = __builtin_amdgcn_readfirstlane(at);
+  end = __builtin_amdgcn_readfirstlane(end);
+  if (threadIdx.x == 0) {
+    if (!NONE) offsets[mine] = at;
+    if (mine + 1 == (uint32_t)experts) offsets[experts] = end;
+  }
+  auto write = [&](int b, uint32_t hits) {
+    if (__ballot(hits != 0) == 0) return;
+    // The lanes' hits of eight steps, summed over the lanes at once: word d holds those of steps d and d + 4 in halves,
+    // where the hits of the steps before are added in (at most 2048 together).
+    uint32_t n = hits - ((hits >> 1) & 0x55555555u), before[4], total[4];
+    n = (n & 0x33333333u) + ((n >> 2) & 0x33333333u);         // four bits per step
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      const uint32_t own = (n >> (4 * d)) & 0x000F000Fu, upto = (uint32_t)wave_scan((int)own);
+      before[d] = upto - own;
+      total[d] = __builtin_amdgcn_readlane((int)upto, 63);
     }
+    uint32_t low = 0, high = (total[0] + total[1] + total[2] + total[3]) & 0xFFFFu;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      before[d] += low | high << 16;
+      low += total[d] & 0xFFFFu;
+      high += total[d] >> 16;
+    }
+    for (uint32_t left = hits; left; left &= left - 1) {      // every lane's next one
+      const int bit = __builtin_ctz(left), step = bit >> 2;
+      const uint32_t even = step & 2 ? before[2] : before[0], odd = step & 2 ? before[3] : before[1];
+      const uint32_t both = step & 1 ? odd : even;
+      const uint32_t nth = (step & 4 ? both >> 16 : both & 0xFFFFu) + __popc((hits >> (4 * step)) & ((1u << (bit & 3)) - 1));
+      order[at + nth] = begin + (8 * b + step) * 256 + (bit & 3);
+    }
+    at += high;
   };
   if constexpr (KEEP) {
 #pragma unroll
-    for (int b = 0; b < kGroupSteps / 8; ++b) {
-      if (8 * b >= steps || __ballot(kept[b] != 0) == 0) continue;
-      // The lanes' hits of eight steps, summed over the lanes at once: ten bits hold the at most 256 hits of a step.
-      int mine3[3], upto[3], total[3];
-#pragma unroll
-      for (int d = 0; d < 3; ++d) {
-        mine3[d] = 0;
-#pragma unroll
-        for (int i = 0; i < 3 && 3 * d + i < 8; ++i) mine3[d] |= __popc((kept[b] >> (4 * (3 * d + i))) & 15u) << (10 * i);
-        upto[d] = wave_scan(mine3[d]);
-        total[d] = __builtin_amdgcn_readlane(upto[d], 63);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int d = i / 3, sh = 10 * (i % 3);
-        put(8 * b + i, (kept[b] >> (4 * i)) & 15u, at + (((upto[d] - mine3[d]) >> sh) & 1023));
-        at += (total[d] >> sh) & 1023;
-      }
-    }
-  } else {
-    for (int i = 0; i < steps; ++i) {
-      uint32_t id[4];
-      load(i, id);
-      uint32_t hits = 0;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) hits |= id[c] == mine ? 1u << c : 0u;
-      const int n = __popc(hits), upto = wave_scan(n);
-      put(i, hits, at + upto - n);
-      at += __builtin_amdgcn_readlane(upto, 63);
-    }
+    for (int b = 0; b < kGroupBatches; ++b) write(b, kept[b]);
+  } else if (same != 0) {
+    for (int b = 0; b < batches; ++b) write(b, look(b));
   }
+  return end;
 }
 
+template <bool KEEP>
+__global__ __launch_bounds__(1024, 8) void group_kernel(const int32_t* __restrict__ sel, int pairs, int experts, int wide,
+                                                        int32_t* __restrict__ offsets, int32_t* __restrict__ order) {
+  __shared__ int less_sh[16], same_sh[16];
+  if ((int)blockIdx.x < experts) {
+    const int end = group_pairs<KEEP, false>(sel, pairs, experts, wide, blockIdx.x, less_sh, same_sh, offsets, order);
+    if ((int)gridDim.x > experts || (int)blockIdx.x + 1 != experts || end == pairs) return;
+    __syncthreads();                                          // the counts in LDS have been read
+  }
+  group_pairs<KEEP, true>(sel, pairs, experts, wide, (uint32_t)experts, less_sh, same_sh, offsets, order);
+}
+
+// A workgroup for each expert and one for the pairs without one, unless that one would be alone in a second round of
+// compute units: then the last expert's looks for them, if there are any (131072 pairs of 256 experts: 10.0 us, 13.9 with
+// the one more; with 2% of the pairs without an expert 19.0 and 17.6).
 hipError_t launch_moe_group(int pairs, int experts, const int32_t* sel, int32_t* offsets, int32_t* order, hipStream_t s) {
   const int wide = (uintptr_t)sel % 16 == 0;
-  const dim3 grid((unsigned)experts + 1), block(1024);
-  if (pairs <= 4096 * kGroupSteps) hipLaunchKernelGGL(group_kernel<true>, grid, block, 0, s, sel, pairs, experts, wide, offsets, order);
+  const dim3 grid((unsigned)experts + (experts % kComputeUnits != 0)), block(1024);
+  if (pairs <= 16 * 2048 * kGroupBatches) hipLaunchKernelGGL(group_kernel<true>, grid, block, 0, s, sel, pairs, experts, wide, offsets, order);
   else hipLaunchKernelGGL(group_kernel<false>, grid, block, 0, s, sel, pairs, experts, wide, offsets, order);
   return hipGetLastError();
 }

@@ -129,6 +129,8 @@ hipError_t launch_prefill_mfma(const uint32_t* codes, const uint16_t* scales, co
 // Element types of the routing and 8-bit entry points (TG_F32, TG_F16, TG_BF16).
 constexpr int kF32 = 0, kF16 = 1, kBf16 = 2;
 
+constexpr int kComputeUnits = 256;       // of the GPU
+
 // Routing of tokens to experts (route.hip).
 constexpr int kRouteMaxExperts = 1024;   // 16 experts in each lane of a wave
 constexpr int kRouteMaxTopK = 64;        // one slot in each lane

@@ -272,35 +272,67 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
         for (int i = 0; i < V; ++i) key[i] = in_kept(kept, i) ? key[i] : 0u;
       }
     }
-    // A round: the wave's largest key, its first holder, one key less.
-    uint32_t my_key = 0;
+    // A round: the wave's largest key, its first holder, one key less. Up to four experts a lane holds in falling order
+    // (equal ones by index: only neighbours change places), so that its first is its largest.
+    constexpr bool kSorted = V <= 4;
+    uint32_t my_key = 0, order = 0;                         // order: the sorted experts' places in the lane, a byte each
+    if constexpr (kSorted) {
+      uint32_t at[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) at[i] = i;
+#pragma unroll
+      for (int n = 1; n < V; ++n)
+#pragma unroll
+        for (int i = n; i > 0; --i) {
+          const bool swap = key[i] > key[i - 1];
+          const uint32_t most_key = max(key[i], key[i - 1]), first = at[i - 1];
+          key[i] = min(key[i], key[i - 1]);
+          key[i - 1] = most_key;
+          at[i - 1] = swap ? at[i] : first;
+          at[i] = swap ? first : at[i];
+        }
+#pragma unroll
+      for (int i = 0; i < V; ++i) order |= at[i] << (8 * i);
+    }
     auto largest = [&]() {
       uint32_t m = key[0];
+      if constexpr (!kSorted) {
 #pragma unroll
-      for (int i = 1; i < V; ++i) m = max(m, key[i]);
+        for (int i = 1; i < V; ++i) m = max(m, key[i]);
+      }
       return wave_max_u32(m);
     };
     auto round = [&](uint32_t top) {
-      bool hit[V], any = false;
-      int first = lane * V;                                 // this lane's first expert with that key
+      int id;
+      if constexpr (kSorted) {
+        const int owner = __builtin_ctzll(__ballot(key[0] == top));
+        id = owner * V + (__builtin_amdgcn_readlane((int)order, owner) & 255);
+        const bool mine = lane == owner;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        hit[i] = key[i] == top;
-        any |= hit[i];
+        for (int i = 0; i < V; ++i) key[i] = mine ? (i + 1 < V ? key[i + 1 < V ? i + 1 : i] : 0u) : key[i];
+        order = mine ? order >> 8 : order;
+      } else {
+        bool hit[V], any = false;
+        int first = lane * V;                               // this lane's first expert with that key
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          hit[i] = key[i] == top;
+          any |= hit[i];
+        }
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i) first = hit[i] ? lane * V + i : first;
+        const int owner = __builtin_ctzll(__ballot(any));
+        id = __builtin_amdgcn_readlane(first, owner);
+        bool open = lane == owner;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          key[i] = open && hit[i] ? 0u : key[i];
+          open = open && !hit[i];
+        }
       }
-#pragma unroll
-      for (int i = V - 1; i >= 0; --i) first = hit[i] ? lane * V + i : first;
-      const int owner = __builtin_ctzll(__ballot(any));
-      const int id = __builtin_amdgcn_readlane(first, owner);
       my_id = lane == found ? id : my_id;
       my_key = lane == found ? top : my_key;
       ++found;
-      bool open = lane == owner;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        key[i] = open && hit[i] ? 0u : key[i];
-        open = open && !hit[i];
-      }
     };
     uint32_t top = 0;
     while (sure && found < a.top_k) {
@@ -420,9 +452,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
 }
 
 // Bound by instruction issue and the rounds' chain of dependent steps: 8192 tokens x 256 experts in 8 groups, top 8, take
-// 14.6 us (681 vector and 386 scalar instructions a token; 15.6 us with an expert read at a time; 8.9 MB, 1.7 us of them),
-// one token of 128 experts 3.4 us. Four tokens share a workgroup where there are many; one each keeps a short batch
-// spread over the card.
+// 11.4 us back to back (627 vector and 331 scalar instructions a token; 12.0 where each round searches a lane's experts
+// anew; 8.9 MB, 1.7 us of them), 65536 tokens 62 us, one token of 128 experts 3.1 us. Four tokens share a workgroup where
+// there are many; one each keeps a short batch spread over the card.
 template <int DT>
 static hipError_t launch_route_t(const RouteArgs& args, hipStream_t s) {
   RouteArgs a = args;

@@ -5,7 +5,7 @@
 // work; an output is rounded three times in binary32 (the sum, and its product with either scale) and once more to a
 // 16-bit output type.
 //
-// What bounds it (MI355X, 2.2 GHz under this load): 4096 x 28672 x 8192 runs at 2440-2530 TOP/s, 61% of what the matrix
+// What bounds it (MI355X, 2.2 GHz under this load): 4096 x 28672 x 8192 runs at 2440-2530 TOP/s, 60-63% of what the matrix
 // cores reach on such values from registers alone (4035 TOP/s; 4900 on zeros: the card's power). The loads to LDS alone
 // take 508 of 789 us with these 256 x 256 tiles, and 722 of 899 with 256 x 128 (373 and 456 where every tile reads the
 // same rows, out of L2); the reads from LDS alone 323. So the way into LDS comes next to the power, and the largest tiles

@@ -177,6 +177,49 @@ def test_named_stream():
         torch.cuda.synchronize()
 
 
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with a workspace of its own."""
+    dev = device()
+    import torch
+    say("int8 and route on two streams at once")
+    L = _layer(torch, dev, 4096, 14336, 40)
+    rows = [_rows(torch, dev, 61, 14336, 41 + i) for i in range(2)]
+    refs = [tg.int8_gemm(L, *r).clone() for r in rows]
+    logits = [torch.randn(3000, 256, generator=torch.Generator().manual_seed(43 + i)).to(dev) for i in range(2)]
+    routed = [tg.moe_route(l, 8) for l in logits]
+    grouped = [tg.moe_group(r[0], 256) for r in routed]
+    ws = [tg.int8_workspace(L, 61) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):
+        got = []
+        for i, st in enumerate(streams):
+            y = tg.int8_gemm(L, *rows[i], ws=ws[i], stream=st)
+            sel, w = tg.moe_route(logits[i], 8, stream=st)
+            got.append((y, sel, w) + tuple(tg.moe_group(sel, 256, stream=st)))
+        for st in streams:
+            st.synchronize()
+        for i in range(2):
+            want = (refs[i],) + tuple(routed[i]) + tuple(grouped[i])
+            assert all(torch.equal(a, b) for a, b in zip(got[i], want))
+
+
+def test_expanded_inputs_refused():
+    """Rows that all lie at one place (a broadcast view) are no layout of these entry points."""
+    dev = device()
+    import torch
+    L = _layer(torch, dev, 64, 256, 50)
+    xq, xs = _rows(torch, dev, 1, 256, 51)
+    with pytest.raises(tg.TgError):
+        tg.int8_gemm(L, xq.expand(4, 256), torch.ones(4, device=dev))
+    with pytest.raises(tg.TgError):
+        tg.int8_quantize(torch.ones(1, 64, device=dev).expand(4, 64))
+    with pytest.raises(tg.TgError):
+        tg.moe_route(torch.ones(1, 64, device=dev).expand(4, 64), 2)
+    with pytest.raises(ValueError):
+        tg.int8_gemm(L, xq.expand(4, 256).contiguous(), torch.ones(1, device=dev).expand(4))
+
+
 def test_route_feeds_the_trellis_block():
     """Router logits of an 8-bit layer -> moe_route -> trellis_moe_block, token by token, against the oracles; a masked router
     leaves slots without an expert, which the block skips."""

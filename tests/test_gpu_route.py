@@ -103,6 +103,25 @@ def test_equal_logits_go_to_the_lowest_index(opts):
     _check(torch, dev, l, 8, opts)
 
 
+@pytest.mark.parametrize("experts", [33, 64, 100, 256, 512, 1000])
+@pytest.mark.parametrize("opts", [{}, dict(sigmoid=True, zero_bias=True), dict(renormalize=False)])
+def test_equal_logits_in_one_lane(experts, opts):
+    """Few values, masked experts between them, and more of the largest than slots: neighbours with equal keys keep their order
+    however many experts a lane holds."""
+    dev = device()
+    import torch
+    say("route ties in a lane", experts, opts)
+    rng = np.random.default_rng(experts)
+    l = rng.integers(0, 3, size=(48, experts)).astype(np.float32)
+    l[rng.random(l.shape) < 0.2] = -np.inf
+    l[0] = 1.0
+    l[1, : experts // 2] = -np.inf
+    opts = dict(opts)
+    if opts.pop("zero_bias", False):
+        opts["bias"] = np.zeros(experts, np.float32)
+    _check(torch, dev, l, 32, opts)
+
+
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_unavailable_experts_and_tokens_without_order(sigmoid):
     """Masked logits (-inf, also whole rows and whole groups), the type's lowest value, NaN and +inf in single tokens."""

@@ -5,16 +5,14 @@
 // work; an output is rounded three times in binary32 (the sum, and its product with either scale) and once more to a
 // 16-bit output type.
 //
-// What bounds it (MI355X, 2.2 GHz under this load): 4096 x 28672 x 8192 runs at 2440-2530 TOP/s, 60-63% of what the matrix
+// What bounds it (MI355X, 2.2 GHz under this load): 4096 x 28672 x 8192 runs at 2440-2550 TOP/s, 60-63% of what the matrix
 // cores reach on such values from registers alone (4035 TOP/s; 4900 on zeros: the card's power). The loads to LDS alone
 // take 508 of 789 us with these 256 x 256 tiles, and 722 of 899 with 256 x 128 (373 and 456 where every tile reads the
 // same rows, out of L2); the reads from LDS alone 323. So the way into LDS comes next to the power, and the largest tiles
 // ask least of it. The library's own 8-bit product takes 844 us there. 1 x 28672 x 8192 reads 235 MB in 42 us (5.6 TB/s; a
-// large copy moves 5.1). 8192 tokens over 128 experts, 1536 x 2048, top 8: 298 us, 220 of them the loads to LDS (187 if
-// the weights of 8 experts serve all), 35 the stores, 42 the first loads and lookups of the 4.5 row tiles of an expert.
-// Leaving out the products of rows that are not there changes nothing (295), workgroups that go on to a next tile and
-// begin its loads before the stores of the last lose (312 -> 320 with 256 x 128 tiles: loads wait for the stores before
-// them).
+// large copy moves 5.1). 8192 tokens over 128 experts, 1536 x 2048, top 8: 269 us; the loads to LDS alone 190, the stores
+// 35-43, the first loads and lookups of short tiles some 40. Workgroups that go on to a next tile and begin its loads
+// before the stores of the last lose (312 -> 320 us with 256 x 128 tiles: loads wait for the stores before them).
 //
 // v_mfma_i32_16x16x64_i8 with the layer's rows as its A operand and the activation rows as its B operand: lane l
 // supplies row l % 16 and the 16 bytes at 16 (l / 16) of 64 bytes of the inner axis on both sides, and ends with four
@@ -272,15 +270,16 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
 #pragma unroll
     for (int r = 0; r < RX; ++r) acc[t][r] = i32x4{0, 0, 0, 0};
   const int slot = 16 * (g ^ S::swizzle(j));     // of the step's first 64 bytes; the h-th 64: slot ^ 64 h
-  const int abase = (wo * 16 * AT + j) * BK + slot, bbase = S::XLDS + (wx * 16 * RX + j) * BK + slot;
+  const int abase = (wo * 16 * AT + j) * BK + slot, bbase = S::XLDS + (wx * 16 + j) * BK + slot;
   // The operands of 64 bytes of the inner axis: read from LDS while the matrix cores work on those before.
   struct Frags {
     i32x4 a[AT], b[RX];
   };
   uint32_t wbuf = 0, xbuf = 0;                   // of step s
-  auto read = [&](Frags& f, int h) {
+  auto read = [&](Frags& f, int h, auto rows) {
 #pragma unroll
-    for (int r = 0; r < RX; ++r) f.b[r] = *reinterpret_cast<const i32x4*>(sh + xbuf + ((bbase ^ (64 * h)) + r * 16 * BK));
+    for (int r = 0; r < decltype(rows)::value; ++r)
+      f.b[r] = *reinterpret_cast<const i32x4*>(sh + xbuf + ((bbase ^ (64 * h)) + r * S::WX * 16 * BK));
 #pragma unroll
     for (int t = 0; t < AT; ++t) f.a[t] = *reinterpret_cast<const i32x4*>(sh + wbuf + ((abase ^ (64 * h)) + t * 16 * BK));
   };
@@ -290,11 +289,11 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
       for (int r = 0; r < RX; ++r) f.b[r] = i32x4{0, 0, 0, 0};
     }
   };
-  auto multiply = [&](const Frags& f) {
+  auto multiply = [&](const Frags& f, auto rows) {
 #pragma unroll
     for (int t = 0; t < AT; ++t)
 #pragma unroll
-      for (int r = 0; r < RX; ++r) acc[t][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[t], f.b[r], acc[t][r], 0, 0, 0);
+      for (int r = 0; r < decltype(rows)::value; ++r) acc[t][r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[t], f.b[r], acc[t][r], 0, 0, 0);
   };
   const int steps_all = (a.n + BK - 1) / BK;
   const int begin = (int)((int64_t)steps_all * sp / a.splits), end = (int)((int64_t)steps_all * (sp + 1) / a.splits);
@@ -305,81 +304,94 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
     wbuf = wbuf == (uint32_t)(ST + EW - 1) * S::WBUF ? 0u : wbuf + S::WBUF;
     xbuf = xbuf == (uint32_t)(ST - 1) * S::XBUF ? 0u : xbuf + S::XBUF;
   };
-  if constexpr (S::AHEAD) {
-    // Loads in the order X(i), W(i + EW): what may still be in flight when X(i) and W(i) are needed.
-    constexpr int kAhead = (EW > 0 ? S::LW : 0) + (ST - 1) * (S::LW + S::LX);
-    if constexpr (EW > 0) load_w(begin, 0);
+  auto main_loop = [&](auto rows) {
+    if constexpr (S::AHEAD) {
+      // Loads in the order X(i), W(i + EW): what may still be in flight when X(i) and W(i) are needed.
+      constexpr int kAhead = (EW > 0 ? S::LW : 0) + (ST - 1) * (S::LW + S::LX);
+      if constexpr (EW > 0) load_w(begin, 0);
 #pragma unroll
-    for (int i = 0; i < ST; ++i) {
-      load_x(min(begin + i, end - 1), i * S::XBUF);
-      load_w(min(begin + i + EW, end - 1), (i + EW) * S::WBUF);
-    }
-    wait_loads<kAhead>();
-    __builtin_amdgcn_s_barrier();
-    read(f[0], 0);
-    // A step: its 64-byte parts in turn, the next part read ahead. Before the next step's first part is read, its loads
-    // have landed and every wave holds this step's last part, so this step's buffers are free for loads.
-    auto step = [&](auto more) {
-#pragma unroll
-      for (int h = 0; h < U; ++h) {
-        if (h == U - 1) {
-          wait_loads<decltype(more)::value ? kAhead - (S::LW + S::LX) : 0>();
-          __builtin_amdgcn_s_barrier();
-          if constexpr (decltype(more)::value) {
-            load_x(s + ST, xbuf);
-            load_w(min(s + ST + EW, end - 1), wbuf);
-          }
-          advance();
-          read(f[(h + 1) & 1], 0);
-        } else {
-          read(f[(h + 1) & 1], h + 1);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(f[h & 1]);
-        __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < ST; ++i) {
+        load_x(min(begin + i, end - 1), i * S::XBUF);
+        load_w(min(begin + i + EW, end - 1), (i + EW) * S::WBUF);
       }
-      if constexpr (U == 1) f[0] = f[1];
-    };
-    for (; s < end - ST; ++s) step(std::true_type{});
-    for (; s < end - 1; ++s) step(std::false_type{});
-    const int left = a.n - s * BK;
-#pragma unroll
-    for (int h = 0; h < U; ++h) {
-      if (h < U - 1) read(f[(h + 1) & 1], h + 1);
-      cut(f[h & 1], h, left);
-      multiply(f[h & 1]);
-    }
-  } else {
-    // Several workgroups share a compute unit: each reads and multiplies in turn, and they fill each other's waits.
-    constexpr int LPS = S::LW + S::LX;
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i) {
-      load_x(min(begin + i, end - 1), i * S::XBUF);
-      load_w(min(begin + i, end - 1), i * S::WBUF);
-    }
-    for (; s < end - (ST - 1); ++s) {
-      wait_loads<(ST - 2) * LPS>();               // step s is in LDS, and this wave is done with step s - 1's buffers
+      wait_loads<kAhead>();
       __builtin_amdgcn_s_barrier();
-      load_x(s + ST - 1, xbuf == 0 ? (ST - 1) * S::XBUF : xbuf - S::XBUF);
-      load_w(s + ST - 1, wbuf == 0 ? (ST - 1) * S::WBUF : wbuf - S::WBUF);
+      read(f[0], 0, rows);
+      // A step: its 64-byte parts in turn, the next part read ahead. Before the next step's first part is read, its loads
+      // have landed and every wave holds this step's last part, so this step's buffers are free for loads.
+      auto step = [&](auto more) {
+#pragma unroll
+        for (int h = 0; h < U; ++h) {
+          if (h == U - 1) {
+            wait_loads<decltype(more)::value ? kAhead - (S::LW + S::LX) : 0>();
+            __builtin_amdgcn_s_barrier();
+            if constexpr (decltype(more)::value) {
+              load_x(s + ST, xbuf);
+              load_w(min(s + ST + EW, end - 1), wbuf);
+            }
+            advance();
+            read(f[(h + 1) & 1], 0, rows);
+          } else {
+            read(f[(h + 1) & 1], h + 1, rows);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          multiply(f[h & 1], rows);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (U == 1) f[0] = f[1];
+      };
+      for (; s < end - ST; ++s) step(std::true_type{});
+      for (; s < end - 1; ++s) step(std::false_type{});
+      const int left = a.n - s * BK;
 #pragma unroll
       for (int h = 0; h < U; ++h) {
-        read(f[0], h);
-        multiply(f[0]);
+        if (h < U - 1) read(f[(h + 1) & 1], h + 1, rows);
+        cut(f[h & 1], h, left);
+        multiply(f[h & 1], rows);
       }
-      advance();
-    }
-    wait_loads<0>();
-    __builtin_amdgcn_s_barrier();
-    for (; s < end; ++s) {
+    } else {
+      // Several workgroups share a compute unit: each reads and multiplies in turn, and they fill each other's waits.
+      constexpr int LPS = S::LW + S::LX;
 #pragma unroll
-      for (int h = 0; h < U; ++h) {
-        read(f[0], h);
-        if (s == end - 1) cut(f[0], h, a.n - s * BK);
-        multiply(f[0]);
+      for (int i = 0; i < ST - 1; ++i) {
+        load_x(min(begin + i, end - 1), i * S::XBUF);
+        load_w(min(begin + i, end - 1), i * S::WBUF);
       }
-      advance();
+      for (; s < end - (ST - 1); ++s) {
+        wait_loads<(ST - 2) * LPS>();               // step s is in LDS, and this wave is done with step s - 1's buffers
+        __builtin_amdgcn_s_barrier();
+        load_x(s + ST - 1, xbuf == 0 ? (ST - 1) * S::XBUF : xbuf - S::XBUF);
+        load_w(s + ST - 1, wbuf == 0 ? (ST - 1) * S::WBUF : wbuf - S::WBUF);
+#pragma unroll
+        for (int h = 0; h < U; ++h) {
+          read(f[0], h, rows);
+          multiply(f[0], rows);
+        }
+        advance();
+      }
+      wait_loads<0>();
+      __builtin_amdgcn_s_barrier();
+      for (; s < end; ++s) {
+#pragma unroll
+        for (int h = 0; h < U; ++h) {
+          read(f[0], h, rows);
+          if (s == end - 1) cut(f[0], h, a.n - s * BK);
+          multiply(f[0], rows);
+        }
+        advance();
+      }
     }
+  };
+  // The rows' tiles of 16 go round the waves, and a wave multiplies all of its own, half or a quarter, as the tile has rows:
+  // the last of an expert's tiles is part empty (8192 tokens over 128 experts 293 -> 278 us with tiles of 256 x 256, 301 ->
+  // 295 and 297 -> 292 with the two of 256 x 128).
+  const int there = ((tile.count + 15) / 16 - wx + S::WX - 1) / S::WX;
+  if constexpr (RX >= 4) {
+    if (there > RX / 2) main_loop(std::integral_constant<int, RX>{});
+    else if (there > RX / 4) main_loop(std::integral_constant<int, RX / 2>{});
+    else main_loop(std::integral_constant<int, RX / 4>{});
+  } else {
+    main_loop(std::integral_constant<int, RX>{});
   }
   wait_loads<0>();
 
@@ -424,7 +436,7 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
   }
 #pragma unroll
   for (int r = 0; r < RX; ++r) {
-    pair[r] = pair_of(a, tile, 16 * (RX * wx + r) + j);
+    pair[r] = pair_of(a, tile, 16 * (S::WX * r + wx) + j);
     xs[r] = a.xs[max(pair[r], 0) / a.pairs_per_row];
   }
   constexpr int N = AT == 1 ? 4 : 8;
@@ -467,22 +479,23 @@ struct TileCost {
   float alone, shared, tile;
 };
 constexpr TileCost kTiles[] = {
-    {256, 256, 1, 1.80f, 1.80f, 5.6f},   // TileShape<4, 8, 4, 2, 128, 2, 1>
-    {256, 128, 1, 1.02f, 1.02f, 4.3f},   // TileShape<4, 4, 4, 2, 128, 3>
-    {256, 128, 2, 1.88f, 2.27f, 2.0f},   // TileShape<4, 4, 4, 2, 64, 3, 0, 4>: two workgroups fill each other's waits
-    {128, 128, 1, 0.60f, 0.60f, 2.0f},   // TileShape<2, 4, 4, 2, 128, 3>
-    {128, 64, 2, 0.344f, 0.79f, 1.7f},    // TileShape<2, 4, 4, 1, 128, 3>
-    {64, 32, 2, 0.13f, 0.25f, 1.15f},    // TileShape<1, 2, 4, 1, 256, 3>
-    {32, 16, 2, 0.042f, 0.132f, 0.64f},   // TileShape<1, 1, 2, 1, 512, 3>
+    {256, 256, 1, 1.484f, 1.484f, 5.05f}, // TileShape<4, 8, 4, 2, 128, 2, 1>
+    {256, 128, 1, 0.974f, 0.974f, 4.26f}, // TileShape<4, 4, 4, 2, 128, 3>
+    {256, 128, 2, 1.10f, 2.15f, 1.8f},    // TileShape<4, 4, 4, 2, 64, 3, 0, 4>: two workgroups fill each other's waits
+    {128, 128, 1, 0.533f, 0.533f, 2.24f}, // TileShape<2, 4, 4, 2, 128, 3>
+    {128, 64, 2, 0.321f, 0.677f, 2.28f},  // TileShape<2, 4, 4, 1, 128, 3>
+    {64, 32, 2, 0.124f, 0.222f, 1.13f},   // TileShape<1, 2, 4, 1, 256, 3>
+    {32, 16, 2, 0.047f, 0.14f, 0.85f},    // TileShape<1, 1, 2, 1, 512, 3>
 };
 constexpr float kStreamRate = 5.3e6f;   // bytes per microsecond of a product that waits for memory alone
 
 // The cheapest shape and split of the inner axis: rounds of workgroups over the compute units, and the time that the
-// bytes take, of which a part is not hidden behind the other. Over the sweep this loses 0.4% against trying everything
-// (12% at worst, 1.4 us of a 9 us product); the best single shape loses 22% on average and a factor of 2.1 at worst, the
-// largest tile a factor of 2.3 and 7.1. A split inner axis costs the parts' sums, so only products with few tiles take
-// one (61 x 4096 x 14336: 19.9 us whole, 14.4 us in two parts; 256 x 28672 x 8192: 76 us whole, 128 us in two).
-// Experts: row tiles as an even routing fills them, one half-filled for each expert.
+// bytes take, of which a part is not hidden behind the other. Over the sweep this loses 0.5% against trying everything
+// (17% at worst, 1.9 us of a 9.4 us product), and 1.1% over 7 sets of experts at 1 to 16384 tokens (22% at worst); the best
+// single shape loses 19% on average and a factor of 2.1 at worst, the largest tile a factor of 1.9 and 6.2. A split inner
+// axis costs the parts' sums, so only products with few tiles take one (64 x 4096 x 14336: 20.2 us whole, 15.6 us in two
+// parts; 256 x 28672 x 8192: 70 us whole, 96 us in two). Experts: row tiles as an even routing fills them, one half-filled
+// for each expert.
 Int8Plan int8_plan(int M, int m, int n, int experts) {
   const float reached = experts > 0 ? (float)(experts < M ? experts : M) : 1.f;
   const float rows = (float)M / reached;

@@ -762,13 +762,6 @@ int32_t check_int8_operands(const Int8Args& a) {
   return TG_OK;
 }
 
-// How wide the outputs of a row can be stored, and the output scales read.
-void set_widths(Int8Args* a) {
-  const size_t four = 4 * type_size(a->out);
-  a->wide_y = a->ldy % 4 != 0 || misaligned(a->y, four) ? 0 : a->ldy % 8 != 0 || misaligned(a->y, 16) ? 1 : 2;
-  a->wide_ws = a->m % 4 == 0 && !misaligned(a->ws, 16);
-}
-
 // The header, a counter for each tile of a product whose inner axis is split, and the parts' sums. The counters lie
 // at one place for every product and are zero between calls; the sums hold anything.
 size_t int8_ws_bytes(int32_t M, int32_t m, int32_t n) {
@@ -852,7 +845,6 @@ TG_API int32_t int8_gemm(int32_t M, int32_t m, int32_t n, const int8_t* xq, int6
   if (st != TG_OK) return st;
   if (!ws || ws_bytes < int8_ws_bytes(M, m, n)) return TG_ERR_WORKSPACE;
   if (misaligned(ws, kAlign)) return TG_ERR_ALIGN;
-  set_widths(&a);
   a.counters = reinterpret_cast<uint32_t*>((char*)ws + kWsHeader);
   a.partials = reinterpret_cast<uint64_t*>((char*)ws + kInt8Partials);
   return launch_status(launch_int8_gemm(a, (hipStream_t)stream));
@@ -887,6 +879,5 @@ TG_API int32_t int8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int3
   if (st != TG_OK) return st;
   if (!offsets || !order) return TG_ERR_NULL;
   if (misaligned(offsets, 4) || misaligned(order, 4)) return TG_ERR_ALIGN;
-  set_widths(&a);
   return launch_status(launch_int8_gemm(a, (hipStream_t)stream));
 }

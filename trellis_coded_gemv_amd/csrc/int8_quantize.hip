@@ -1,5 +1,6 @@
 // 8-bit rows with a scale for each row. Bound by memory: 4096 rows of 14336 bf16 values (117 MB in, 59 MB out) take 30
-// us, 5.9 TB/s, where a large copy moves 5.1; reading a row twice took 105 us. One row of 8192 takes 2.7 us.
+// us, 5.9 TB/s, where a large copy moves 5.1; reading a row twice took 105 us. Rows of 14335, none of them aligned: 40 us (72
+// read value by value). One row of 8192 takes 2.7 us.
 #include "tg_device.hpp"
 #include "tg_internal.hpp"
 
@@ -53,8 +54,8 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top, float* scale) {
   return r;
 }
 
-// Rows whose 16-byte pieces are aligned: the row stays in registers between the two passes, PER pieces to a thread,
-// and is read once.
+// Rows of up to PER * THREADS 16-byte pieces, at any address: the row stays in registers between the two passes, PER
+// pieces to a thread, and is read once.
 template <int DT, int THREADS, int PER>
 __global__ __launch_bounds__(THREADS) void quantize_rows_kernel(const void* __restrict__ x, int64_t ldx,
                                                                 int8_t* __restrict__ q, int64_t ldq,
@@ -71,8 +72,8 @@ __global__ __launch_bounds__(THREADS) void quantize_rows_kernel(const void* __re
     const int c = threadIdx.x + THREADS * i;
     v[i] = u32x4{0, 0, 0, 0};
     if (c < pieces) {
-      if constexpr (DT == kF32) v[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const float*>(x) + base + c * VEC);
-      else v[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + base + c * VEC);
+      if constexpr (DT == kF32) v[i] = *reinterpret_cast<const u32x4_any*>(reinterpret_cast<const float*>(x) + base + c * VEC);
+      else v[i] = *reinterpret_cast<const u32x4_any*>(reinterpret_cast<const uint16_t*>(x) + base + c * VEC);
     }
   }
   float last = 0.f;                                        // the row's end, short of a piece: one value to a thread
@@ -117,17 +118,17 @@ __global__ __launch_bounds__(THREADS) void quantize_rows_kernel(const void* __re
       }
       w[h] = (((uint32_t)b[0] & 255u) | ((uint32_t)b[1] & 255u) << 8 | ((uint32_t)b[2] & 255u) << 16 | (uint32_t)b[3] << 24) & keep;
     }
-    if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(qr + c * VEC) = w[0];
-    else *reinterpret_cast<u32x2*>(qr + c * VEC) = u32x2{w[0], w[1]};
+    if constexpr (VEC == 4) *reinterpret_cast<u32_any*>(qr + c * VEC) = w[0];
+    else *reinterpret_cast<u32x2_any*>(qr + c * VEC) = u32x2_any{w[0], w[1]};
   }
   if ((int)threadIdx.x < rest) qr[pieces * VEC + threadIdx.x] = r.finite ? (int8_t)quantize_step(last, r.inv) : (int8_t)0;
 }
 
-// Rows of any alignment and length, read twice.
-template <int DT, int THREADS>
-__global__ __launch_bounds__(THREADS) void quantize_any_kernel(const void* __restrict__ x, int64_t ldx,
-                                                               int8_t* __restrict__ q, int64_t ldq,
-                                                               float* __restrict__ scales, int n, int rows) {
+// Longer rows, read twice.
+template <int DT>
+__global__ __launch_bounds__(1024) void quantize_long_kernel(const void* __restrict__ x, int64_t ldx, int8_t* __restrict__ q,
+                                                             int64_t ldq, float* __restrict__ scales, int n, int rows) {
+  constexpr int THREADS = 1024;
   __shared__ uint32_t wmax[THREADS / 64];
   const int row = blockIdx.y * gridDim.x + blockIdx.x;
   if (row >= rows) return;
@@ -168,14 +169,10 @@ template <int DT>
 static hipError_t launch_quantize_t(int rows, int n, const void* x, int64_t ldx, int8_t* q, int64_t ldq, float* scales,
                                     hipStream_t s) {
   constexpr int VEC = DT == kF32 ? 4 : 8;
-  const bool aligned = (uintptr_t)x % 16 == 0 && (uintptr_t)q % VEC == 0 &&
-                       (rows == 1 || (ldx % VEC == 0 && ldq % VEC == 0));
   const int pieces = n / VEC;
-  if (aligned && pieces <= 256 && pieces >= 1) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
-  else if (aligned && pieces <= 4 * 256 && rows >= 512) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
-  else if (aligned && pieces <= 8 * 1024 && pieces >= 1) launch_quantize_rows<DT, 1024>(rows, n, x, ldx, q, ldq, scales, s);
-  else if (n <= 1024) hipLaunchKernelGGL((quantize_any_kernel<DT, 256>), row_grid(rows), dim3(256), 0, s, x, ldx, q, ldq, scales, n, rows);
-  else hipLaunchKernelGGL((quantize_any_kernel<DT, 1024>), row_grid(rows), dim3(1024), 0, s, x, ldx, q, ldq, scales, n, rows);
+  if (pieces <= 256 || (pieces <= 4 * 256 && rows >= 512)) launch_quantize_rows<DT, 256>(rows, n, x, ldx, q, ldq, scales, s);
+  else if (pieces <= 8 * 1024) launch_quantize_rows<DT, 1024>(rows, n, x, ldx, q, ldq, scales, s);
+  else hipLaunchKernelGGL(quantize_long_kernel<DT>, row_grid(rows), dim3(1024), 0, s, x, ldx, q, ldq, scales, n, rows);
   return hipGetLastError();
 }
 

@@ -48,18 +48,29 @@ __device__ __forceinline__ float logit(const void* p, int64_t i) {
   return __builtin_bit_cast(float, (uint32_t)b << 16);
 }
 
-// V neighbouring values at a multiple of their size, up to 16 bytes at once.
+// V neighbouring values, up to 16 bytes at once.
 template <int V, int DT>
 __device__ __forceinline__ void load_neighbours(const void* p, int64_t at, float (&f)[V]) {
   constexpr int kBytes = V * (DT == kF32 ? 4 : 2), kWords = kBytes >= 16 ? 4 : kBytes / 4;
   if constexpr (kWords == 0) {
     f[0] = logit<DT>(p, at);
   } else {
-    typedef uint32_t words __attribute__((ext_vector_type(kWords)));
     constexpr int kEach = kWords * (DT == kF32 ? 1 : 2);    // values of one load
 #pragma unroll
     for (int d = 0; d < V / kEach; ++d) {
-      const words w = *reinterpret_cast<const words*>(reinterpret_cast<const char*>(p) + (at + d * kEach) * (DT == kF32 ? 4 : 2));
+      const char* from = reinterpret_cast<const char*>(p) + (at + d * kEach) * (DT == kF32 ? 4 : 2);
+      uint32_t w[4];
+      if constexpr (kWords == 4) {
+        const u32x4_any v = *reinterpret_cast<const u32x4_any*>(from);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = v[i];
+      } else if constexpr (kWords == 2) {
+        const u32x2_any v = *reinterpret_cast<const u32x2_any*>(from);
+        w[0] = v[0];
+        w[1] = v[1];
+      } else {
+        w[0] = *reinterpret_cast<const u32_any*>(from);
+      }
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const uint32_t word = w[DT == kF32 ? i : i / 2];
@@ -176,7 +187,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
   const float inf = __builtin_huge_valf();
   float l[V], bias[V];
   const int64_t at0 = (int64_t)token * a.ld;
-  if (a.whole) {            // a lane's experts are all there, or none, and lie at a multiple of their size
+  if (a.experts % V == 0) { // a lane's experts are all there, or none
     const int e = min(lane * V, a.experts - V);
     load_neighbours<V, DT>(a.logits, at0 + e, l);
     if (a.bias) load_neighbours<V, kF32>(a.bias, e, bias);
@@ -456,14 +467,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
 // anew; 8.9 MB, 1.7 us of them), 65536 tokens 62 us, one token of 128 experts 3.1 us. Four tokens share a workgroup where
 // there are many; one each keeps a short batch spread over the card.
 template <int DT>
-static hipError_t launch_route_t(const RouteArgs& args, hipStream_t s) {
-  RouteArgs a = args;
+static hipError_t launch_route_t(const RouteArgs& a, hipStream_t s) {
   const int waves = a.tokens >= 1024 ? kRouteWaves : 1;
   const dim3 grid((unsigned)((a.tokens + waves - 1) / waves)), block(64 * waves);
   const int v = a.experts <= 64 ? 1 : a.experts <= 128 ? 2 : a.experts <= 256 ? 4 : a.experts <= 512 ? 8 : 16;
-  const size_t each = DT == kF32 ? 4 : 2, bytes = v * each < 16 ? v * each : 16;
-  a.whole = a.experts % v == 0 && (uintptr_t)a.logits % bytes == 0 && (a.tokens == 1 || a.ld * each % bytes == 0) &&
-            (!a.bias || (uintptr_t)a.bias % (v * 4 < 16 ? v * 4 : 16) == 0);
   if (v == 1) hipLaunchKernelGGL((route_kernel<1, DT>), grid, block, 0, s, a);
   else if (v == 2) hipLaunchKernelGGL((route_kernel<2, DT>), grid, block, 0, s, a);
   else if (v == 4) hipLaunchKernelGGL((route_kernel<4, DT>), grid, block, 0, s, a);
@@ -499,7 +506,7 @@ __device__ __forceinline__ uint32_t twice_plus(uint32_t v, uint64_t mask) {
 // The pairs of expert `mine` (NONE: mine == experts, those without one) -> their places, and where they end. KEEP: a
 // wave's batches fit kGroupBatches; else they are looked at again for the writing.
 template <bool KEEP, bool NONE>
-__device__ __forceinline__ int group_pairs(const int32_t* __restrict__ sel, int pairs, int experts, int wide, uint32_t mine,
+__device__ __forceinline__ int group_pairs(const int32_t* __restrict__ sel, int pairs, int experts, uint32_t mine,
                                            int (&less_sh)[16], int (&same_sh)[16], int32_t* __restrict__ offsets,
                                            int32_t* __restrict__ order) {
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -509,10 +516,10 @@ __device__ __forceinline__ int group_pairs(const int32_t* __restrict__ sel, int 
   int less = 0;
   auto look = [&](int b) {
     uint32_t hits = 0;
-    if (wide && 8 * b + 8 <= steps && stretch + (8 * b + 8) * 256 <= pairs) {
+    if (8 * b + 8 <= steps && stretch + (8 * b + 8) * 256 <= pairs) {
       u32x4 v[8];                                             // eight loads in flight
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4*>(sel + begin + (8 * b + i) * 256);
+      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4_any*>(sel + begin + (8 * b + i) * 256);
       // A hit is doubled into its place by the addition that adds it: the first of 32 ends on top.
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -605,25 +612,24 @@ __device__ __forceinline__ int group_pairs(const int32_t* __restrict__ sel, int 
 }
 
 template <bool KEEP>
-__global__ __launch_bounds__(1024, 8) void group_kernel(const int32_t* __restrict__ sel, int pairs, int experts, int wide,
+__global__ __launch_bounds__(1024, 8) void group_kernel(const int32_t* __restrict__ sel, int pairs, int experts,
                                                         int32_t* __restrict__ offsets, int32_t* __restrict__ order) {
   __shared__ int less_sh[16], same_sh[16];
   if ((int)blockIdx.x < experts) {
-    const int end = group_pairs<KEEP, false>(sel, pairs, experts, wide, blockIdx.x, less_sh, same_sh, offsets, order);
+    const int end = group_pairs<KEEP, false>(sel, pairs, experts, blockIdx.x, less_sh, same_sh, offsets, order);
     if ((int)gridDim.x > experts || (int)blockIdx.x + 1 != experts || end == pairs) return;
     __syncthreads();                                          // the counts in LDS have been read
   }
-  group_pairs<KEEP, true>(sel, pairs, experts, wide, (uint32_t)experts, less_sh, same_sh, offsets, order);
+  group_pairs<KEEP, true>(sel, pairs, experts, (uint32_t)experts, less_sh, same_sh, offsets, order);
 }
 
 // A workgroup for each expert and one for the pairs without one, unless that one would be alone in a second round of
 // compute units: then the last expert's looks for them, if there are any (131072 pairs of 256 experts: 10.0 us, 13.9 with
 // the one more; with 2% of the pairs without an expert 19.0 and 17.6).
 hipError_t launch_moe_group(int pairs, int experts, const int32_t* sel, int32_t* offsets, int32_t* order, hipStream_t s) {
-  const int wide = (uintptr_t)sel % 16 == 0;
   const dim3 grid((unsigned)experts + (experts % kComputeUnits != 0)), block(1024);
-  if (pairs <= 16 * 2048 * kGroupBatches) hipLaunchKernelGGL(group_kernel<true>, grid, block, 0, s, sel, pairs, experts, wide, offsets, order);
-  else hipLaunchKernelGGL(group_kernel<false>, grid, block, 0, s, sel, pairs, experts, wide, offsets, order);
+  if (pairs <= 16 * 2048 * kGroupBatches) hipLaunchKernelGGL(group_kernel<true>, grid, block, 0, s, sel, pairs, experts, offsets, order);
+  else hipLaunchKernelGGL(group_kernel<false>, grid, block, 0, s, sel, pairs, experts, offsets, order);
   return hipGetLastError();
 }
 

@@ -142,7 +142,6 @@ struct RouteArgs {
   int64_t ld;
   int32_t tokens, experts, top_k, n_group, topk_group, group_top;
   int32_t sigmoid, renorm;
-  int32_t whole;          // a lane's experts can be read at once (set by the launch)
   float scale;
 };
 hipError_t launch_moe_route(const RouteArgs& a, int dtype, hipStream_t s);
@@ -161,8 +160,6 @@ struct Int8Args {
   int32_t M, m, n;        // M: output rows (pairs)
   int32_t experts, pairs_per_row;
   int32_t out;            // kF32, kF16, kBf16
-  int32_t wide_y;         // 1: four neighbouring outputs of a row can be stored at once; 2: eight of 16 bits
-  int32_t wide_ws;        // four neighbouring output scales can be read at once
   int32_t splits;         // parts of the inner axis (dense only)
   uint32_t* counters;     // a tile's arrivals, zero between calls
   uint64_t* partials;     // [tiles][splits] sums of a workgroup's lanes

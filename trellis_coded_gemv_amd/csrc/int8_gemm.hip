@@ -167,12 +167,13 @@ int row_tiles(const Int8Args& a, int rows_per_tile) {
 }
 
 // 16 bytes of global memory per lane to LDS at base + 16 * lane (base wave-uniform): from a lane's own address, or from
-// a lane's offset to a wave-uniform address.
+// a lane's offset to a wave-uniform address. The load reads m0 one wait state after a scalar write of it at the earliest,
+// which the compiler does not see to inside inline assembly (its builtin would, but waits for the loads at every LDS read).
 __device__ __forceinline__ void load_to_lds(const int8_t* p, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_base), "v"(p) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds_base), "v"(p) : "m0", "memory");
 }
 __device__ __forceinline__ void load_to_lds(const int8_t* p, uint32_t offset, uint32_t lds_base) {
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(offset), "s"(p) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds_base), "v"(offset), "s"(p) : "m0", "memory");
 }
 
 // Wait until at most N of this wave's loads are in flight and its LDS reads are done.

@@ -224,18 +224,12 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
   }
   const int size = a.experts / a.n_group;
   auto there = [&](int i) { return l[i] != -inf && bias[i] != -inf; };
-  // The groups' ranks by value -> the kept ones as bits, and whether the border is wider than `tol` of the values.
-  auto keep = [&](auto value, float tol, float rel, bool& clear) {
+  // The groups' ranks by value -> the kept ones as bits.
+  auto keep = [&](auto value) {
     int before = 0;
     for (int i = 0; i < a.n_group; ++i) {
       const auto v = lane_value(value, i);
       before += v > value || (v == value && i < lane) ? 1 : 0;
-    }
-    const uint64_t last = __ballot(lane < a.n_group && before == a.topk_group - 1);
-    const uint64_t next = __ballot(lane < a.n_group && before == a.topk_group);
-    if (next) {
-      const auto in = lane_value(value, __builtin_ctzll(last)), out = lane_value(value, __builtin_ctzll(next));
-      clear = out == (decltype(out))kNone || in - out > tol + rel * fabs(in);
     }
     return __ballot(lane < a.n_group && before < a.topk_group);
   };
@@ -276,9 +270,20 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
       }
       if (a.n_group > 1) {
         const Best2<uint32_t> best = group_best<V, uint32_t>(rank, 0u, reinterpret_cast<uint32_t*>(place[wave]), lane, size, a.n_group);
-        const float value = best.first == 0 ? -inf
-                            : unordered(best.first) + (a.group_top == 2 && best.second != 0 ? unordered(best.second) : 0.f);
-        const uint64_t kept = keep(value, 0x1p-17f, 0x1p-21f, sure);
+        const bool none = best.first == 0;
+        const float one = none ? -inf : unordered(best.first);
+        const float two = a.group_top == 2 && best.second != 0 ? unordered(best.second) : 0.f;
+        const float value = one + two;
+        const uint64_t kept = keep(value);
+        if (a.topk_group < a.n_group) {
+          // A value is off by less than its two scores' 2^-18, and each of its roundings (the two keys, their sum, this
+          // bound) by 2^-24 of what the keys amount to, which may be far more than their sum.
+          const float off = 0x1p-18f + 0x1p-22f * (fabsf(one) + fabsf(two));
+          const bool in = (kept >> lane) & 1;
+          const float least = -wave_max_f32(in && !none ? off - value : -inf);        // of any kept group
+          const float most_left = wave_max_f32(!in && !none ? value + off : -inf);    // of any other
+          sure = least > most_left;
+        }
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = in_kept(kept, i) ? key[i] : 0u;
       }
@@ -389,9 +394,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
     for (int i = 0; i < V; ++i) key[i] = there(i) ? score[i] + (double)bias[i] : kNone;
     uint64_t kept = ~0ull;
     if (a.n_group > 1) {
-      bool clear;
       const Best2<double> best = group_best<V, double>(key, kNone, place[wave], lane, size, a.n_group);
-      kept = keep(a.group_top == 2 && best.second != kNone ? best.first + best.second : best.first, 0.f, 0.f, clear);
+      kept = keep(a.group_top == 2 && best.second != kNone ? best.first + best.second : best.first);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {

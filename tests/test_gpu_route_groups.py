@@ -1,4 +1,4 @@
-"""moe_route within groups where a group's value is not what its binary32 sum says: biases that cancel."""
+"""moe_route within groups where a group's value is not what its binary32 sum says: biases that cancel, and biases whose sums leave the type."""
 import numpy as np
 import pytest
 
@@ -50,3 +50,23 @@ def test_a_far_group_of_large_biases(B, experts, n_group):
         bias[size + 2:2 * size] = bias[3 * size + 2:4 * size] = -2 * B      # so that -B is their second largest
     for topk_group in (1, 2, n_group - 1, n_group):
         _check(torch, dev, l, 2, bias, sigmoid=True, n_group=n_group, topk_group=topk_group, group_top=2)
+
+
+LOW, INF = float(np.finfo(np.float32).min), float("inf")
+
+
+@pytest.mark.parametrize("bias", [
+    [-INF, -INF, -3.4e38, -3.4e38], [-3.4e38, -3.4e38, -INF, -INF], [-INF, -INF, LOW, LOW, -INF, -INF, LOW, LOW], [LOW, LOW, -3.3e38, LOW],
+    [LOW, LOW, LOW, LOW], [LOW, -INF, LOW, LOW, -INF, LOW, 0.0, LOW], [3.4e38, 3.4e38, 3.3e38, 3.4e38], [3.2e38, 3.3e38, 3.3e38, 3.3e38],
+    [-LOW, LOW, 0.0, 0.0], [-INF, -LOW, -LOW, LOW, LOW, LOW, -INF, -INF]])
+@pytest.mark.parametrize("group_top", [1, 2])
+def test_values_that_leave_binary32(bias, group_top):
+    """Sums of two lowest (or largest) biases are infinite in binary32 and numbers in binary64; groups without experts beside them."""
+    dev = device()
+    import torch
+    say("route groups lowest", bias, group_top)
+    rng = np.random.default_rng(7)
+    l = rng.normal(size=(40, len(bias))).astype(np.float32)
+    for topk_group in range(1, len(bias) // 2 + 1):
+        for sigmoid in (True, False):
+            _check(torch, dev, l, 2, np.array(bias, np.float32), sigmoid=sigmoid, n_group=len(bias) // 2, topk_group=topk_group, group_top=group_top)

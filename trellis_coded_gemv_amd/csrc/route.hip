@@ -277,11 +277,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
         const uint64_t kept = keep(value);
         if (a.topk_group < a.n_group) {
           // A value is off by less than its two scores' 2^-18, and each of its roundings (the two keys, their sum, this
-          // bound) by 2^-24 of what the keys amount to, which may be far more than their sum.
-          const float off = 0x1p-18f + 0x1p-22f * (fabsf(one) + fabsf(two));
+          // bound) by 2^-24 of what the keys amount to, which may be far more than their sum. Keys that leave binary32
+          // together say nothing of theirs.
+          const float both = fabsf(one) + fabsf(two);
+          const float off = both < inf ? 0x1p-18f + 0x1p-22f * both : inf, at = both < inf ? value : 0.f;
           const bool in = (kept >> lane) & 1;
-          const float least = -wave_max_f32(in && !none ? off - value : -inf);        // of any kept group
-          const float most_left = wave_max_f32(!in && !none ? value + off : -inf);    // of any other
+          const float least = -wave_max_f32(in && !none ? off - at : -inf);       // of any kept group with experts
+          const float most_left = wave_max_f32(!in && !none ? at + off : -inf);   // of any other
           sure = least > most_left;
         }
 #pragma unroll

@@ -224,9 +224,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
   }
   const int size = a.experts / a.n_group;
   auto there = [&](int i) { return l[i] != -inf && bias[i] != -inf; };
-  // The groups' ranks by value -> the kept ones as bits.
-  auto keep = [&](auto value) {
-    int before = 0;
+  // How many groups stand before a lane's by value, those of lower index among equal ones -> the kept ones as bits.
+  auto keep = [&](auto value, int& before) {
+    before = 0;
     for (int i = 0; i < a.n_group; ++i) {
       const auto v = lane_value(value, i);
       before += v > value || (v == value && i < lane) ? 1 : 0;
@@ -274,17 +274,24 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
         const float one = none ? -inf : unordered(best.first);
         const float two = a.group_top == 2 && best.second != 0 ? unordered(best.second) : 0.f;
         const float value = one + two;
-        const uint64_t kept = keep(value);
+        int before;
+        const uint64_t kept = keep(value, before);
         if (a.topk_group < a.n_group) {
           // A value is off by less than its two scores' 2^-18, and each of its roundings (the two keys, their sum, this
           // bound) by 2^-24 of what the keys amount to, which may be far more than their sum. Keys that leave binary32
           // together say nothing of theirs.
           const float both = fabsf(one) + fabsf(two);
-          const float off = both < inf ? 0x1p-18f + 0x1p-22f * both : inf, at = both < inf ? value : 0.f;
-          const bool in = (kept >> lane) & 1;
-          const float least = -wave_max_f32(in && !none ? off - at : -inf);       // of any kept group with experts
-          const float most_left = wave_max_f32(!in && !none ? at + off : -inf);   // of any other
-          sure = least > most_left;
+          if (__ballot(!none && !(both < 4.f)) == 0) {      // biases of a score's size: only the border is looked at
+            const int last = __builtin_ctzll(__ballot(before == a.topk_group - 1));
+            const int next = __builtin_ctzll(__ballot(before == a.topk_group));
+            sure = !(lane_value(value, last) - lane_value(value, next) <= 2 * (0x1p-18f + 0x1p-20f));
+          } else {
+            const float off = both < inf ? 0x1p-18f + 0x1p-22f * both : inf, at = both < inf ? value : 0.f;
+            const bool in = (kept >> lane) & 1;
+            const float least = -wave_max_f32(in && !none ? off - at : -inf);       // of any kept group with experts
+            const float most_left = wave_max_f32(!in && !none ? at + off : -inf);   // of any other
+            sure = least > most_left;
+          }
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) key[i] = in_kept(kept, i) ? key[i] : 0u;
@@ -396,8 +403,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
     for (int i = 0; i < V; ++i) key[i] = there(i) ? score[i] + (double)bias[i] : kNone;
     uint64_t kept = ~0ull;
     if (a.n_group > 1) {
+      int before;
       const Best2<double> best = group_best<V, double>(key, kNone, place[wave], lane, size, a.n_group);
-      kept = keep(a.group_top == 2 && best.second != kNone ? best.first + best.second : best.first);
+      kept = keep(a.group_top == 2 && best.second != kNone ? best.first + best.second : best.first, before);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {

@@ -534,11 +534,15 @@ int32_t int8_gemm(int32_t M, int32_t m, int32_t n, const int8_t *xq, int64_t ldx
 /* Workspace bytes for int8_gemm (0 if the shape is invalid). */
 size_t tg_int8_workspace_size(int32_t M, int32_t m, int32_t n);
 
+/* Added to int8_gemm_grouped's out_dtype: rows of Y without an expert are set to zero. */
+#define TG_ZERO_UNROUTED 0x100
+
 /*
  * The experts' products over routed pairs (moe_group's order and offsets), in one launch:
  *     Y[p, o] = (sum_i xq[t, i] * wq[e, o, i]) * xs[t] * wscales[e, o],  t = p / pairs_per_row,
  * for every pair p = order[j] of expert e, offsets[e] <= j < offsets[e + 1]. Rows of Y whose pair belongs
- * to no expert are left as they were. pairs_per_row = top_k reads one activation row for all experts of a
+ * to no expert are left as they were; with TG_ZERO_UNROUTED in out_dtype, those of the pairs that order lists
+ * behind offsets[experts] (moe_route's slots with id -1) are set to zero. pairs_per_row = top_k reads one activation row for all experts of a
  * token (gate and up); 1 reads a row for each pair (down).
  *   pairs : 1 .. 2^20, a multiple of pairs_per_row; experts : 1 .. 1024; m, n : as for int8_gemm.
  *   xq    : device, pairs / pairs_per_row rows, as for int8_gemm; xs : device, as many fp32.

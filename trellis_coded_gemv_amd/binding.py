@@ -36,6 +36,7 @@ EXPORTS = ("tg_abi_version", "tg_build_id", "tg_workspace_status", "tg_status_st
 
 TG_ROUTE_SIGMOID = 1
 TG_ROUTE_RENORM = 2
+TG_ZERO_UNROUTED = 0x100
 
 
 class TgLayer(ctypes.Structure):
@@ -660,7 +661,8 @@ def int8_gemm(layer: "Int8Layer", xq, xs, Y=None, out_dtype=None, ws=None, strea
 
 def int8_gemm_grouped(experts: "Int8Experts", xq, xs, offsets, order, pairs_per_row: int = 1, Y=None, out_dtype=None, stream=None):
     """Y [pairs, m]: row p = order[j], offsets[e] <= j < offsets[e + 1], is expert e's product with the 8-bit row
-    xq[p // pairs_per_row]. Rows of pairs without an expert are left as they were: pass a zeroed Y where there are any."""
+    xq[p // pairs_per_row]. Rows of pairs without an expert, which order lists behind offsets[-1], are zero in an output that
+    the call makes, and left as they were in a Y of the caller's."""
     torch = _torch()
     w = "int8_gemm_grouped"
     m, n, count = experts.m, experts.n, experts.experts
@@ -674,9 +676,10 @@ def int8_gemm_grouped(experts: "Int8Experts", xq, xs, offsets, order, pairs_per_
     if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
             return int8_gemm_grouped(experts, xq, xs, offsets, order, pairs_per_row, Y, out_dtype)
+    zero = TG_ZERO_UNROUTED if Y is None else 0
     Y, code, ldy = _int8_out(torch, w, Y, pairs, m, out_dtype, xq)
     status = (_lib or lib()).int8_gemm_grouped(pairs, count, m, n, xq.data_ptr(), ldx, xs.data_ptr(), int(pairs_per_row), experts.q.data_ptr(),
-                                   experts.scales.data_ptr(), offsets.data_ptr(), order.data_ptr(), Y.data_ptr(), code, ldy,
+                                   experts.scales.data_ptr(), offsets.data_ptr(), order.data_ptr(), Y.data_ptr(), code | zero, ldy,
                                    torch._C._cuda_getCurrentRawStream(at))
     if status:
         raise TgError(status, w)

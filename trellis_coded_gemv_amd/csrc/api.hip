@@ -874,7 +874,8 @@ TG_API int32_t int8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int3
   a.n = n;
   a.experts = experts;
   a.pairs_per_row = pairs_per_row;
-  a.out = out_dtype;
+  a.out = out_dtype & ~TG_ZERO_UNROUTED;
+  a.zero_rest = (out_dtype & TG_ZERO_UNROUTED) != 0;
   st = check_int8_operands(a);
   if (st != TG_OK) return st;
   if (!offsets || !order) return TG_ERR_NULL;

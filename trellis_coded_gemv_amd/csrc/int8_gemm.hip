@@ -30,14 +30,15 @@ typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 // A workgroup's tile. rows: dense, output rows first .. first + count - 1; experts, places first .. of order.
 struct Tile {
   int ot, rt, sp;             // output tile, row tile, part of the inner axis
-  int expert, first, count;   // count 0: nothing to do
+  int expert, first, count;   // expert -1: rows to set to zero; count 0: nothing to do
 };
 
 // Workgroup -> tile. Workgroups b, b + 8, ... share an XCD and its L2: each XCD takes a run of neighbouring tiles out of
 // those that there are, the same number for each. Dense: 8 row tiles by all output tiles, rows first, so that an XCD's
 // resident workgroups share a few row tiles and output tiles. Experts: the row tiles are numbered expert by expert (every
 // wave finds them from the offsets, up to 16 neighbouring experts to a lane), outputs first, so that an expert's tiles
-// stay together; the launch holds the most tiles that the pairs could need, and what is over ends at once.
+// stay together; behind them, where they are to be set to zero, the pairs without an expert; the launch holds the most
+// tiles that the pairs could need, and what is over ends at once.
 // Every value is wave-uniform.
 __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int row_tiles, int rows_per_tile) {
   constexpr int kHeld = 4;                      // experts of a lane whose places are kept
@@ -45,6 +46,7 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
   const int lane = threadIdx.x & 63;
   const int per_lane = (a.experts + 63) >> 6;
   int at[kHeld + 1], mine = 0, scan = 0;        // where a lane's experts begin, and the one behind them
+  int routed = 0;                               // row tiles of the experts
   // Past the last expert: where it ends, so none of its own. Places are cut to [0, M].
   auto place = [&](int e) { return min(max(a.offsets[min(e, a.experts)], 0), a.M); };
   auto tiles = [&](int from, int to) { return to > from ? (to - from + rows_per_tile - 1) / rows_per_tile : 0; };
@@ -58,7 +60,8 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
       for (int i = 0; i < per_lane; ++i) mine += tiles(place(lane * per_lane + i), place(lane * per_lane + i + 1));
     }
     scan = wave_scan(mine);
-    row_tiles = min(row_tiles, __builtin_amdgcn_readlane(scan, 63));
+    routed = __builtin_amdgcn_readlane(scan, 63);
+    row_tiles = min(row_tiles, routed + (a.zero_rest ? tiles(__builtin_amdgcn_readfirstlane(place(a.experts)), a.M) : 0));
   }
   int id;
   {
@@ -83,6 +86,12 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
   }
   t.rt = id / out_tiles;
   t.ot = id - t.rt * out_tiles;
+  if (t.rt >= routed) {
+    t.expert = -1;
+    t.first = __builtin_amdgcn_readfirstlane(place(a.experts)) + (t.rt - routed) * rows_per_tile;
+    t.count = min(rows_per_tile, a.M - t.first);
+    return t;
+  }
   const int owner = __builtin_ctzll(__ballot(scan > t.rt));     // some lane is, as rt < the last lane's sum
   int left = t.rt - __builtin_amdgcn_readlane(scan - mine, owner);
   for (int i = 0; i < per_lane; ++i) {
@@ -159,11 +168,12 @@ __device__ __forceinline__ void store_outputs(void* y, int64_t at, const float (
 namespace {
 
 // Row tiles of a launch: exact for a dense product; for the experts' an upper bound that holds for every way the
-// pairs can fall (each expert with pairs leaves at most one tile part-filled).
+// pairs can fall (each expert with pairs leaves at most one tile part-filled, and so do the pairs without one).
 int row_tiles(const Int8Args& a, int rows_per_tile) {
   const int full = (a.M + rows_per_tile - 1) / rows_per_tile;
   if (!a.offsets) return full;
-  return a.M / rows_per_tile + (a.experts < a.M ? a.experts : a.M);
+  const int lists = a.experts + (a.zero_rest ? 1 : 0);
+  return a.M / rows_per_tile + (lists < a.M ? lists : a.M);
 }
 
 // 16 bytes of global memory per lane to LDS at base + 16 * lane (base wave-uniform): from a lane's own address, or from
@@ -225,6 +235,14 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
   if (tile.count <= 0) return;
   const int ot = tile.ot, rt = tile.rt, sp = tile.sp;
   const int o0 = ot * TO;
+  if (tile.expert < 0) {                         // eight neighbouring outputs to a thread
+    const float zeros[8] = {};
+    for (int i = threadIdx.x; i < tile.count * (TO / 8); i += 64 * NW) {
+      const int pair = pair_of(a, tile, i / (TO / 8)), o = o0 + i % (TO / 8) * 8;
+      if (pair >= 0 && o < a.m) store_outputs<DT, 8>(a.y, (int64_t)pair * a.ldy + o, zeros, a.m - o);
+    }
+    return;
+  }
   const int wo = wave % S::WO, wx = wave / S::WO;
 
   // Loads: an instruction fills RPI rows of LDS; lane l the slot l % (BK / 16) of row l / (BK / 16), where the piece

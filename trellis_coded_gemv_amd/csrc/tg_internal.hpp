@@ -161,6 +161,7 @@ struct Int8Args {
   int32_t experts, pairs_per_row;
   int32_t out;            // kF32, kF16, kBf16
   int32_t splits;         // parts of the inner axis (dense only)
+  int32_t zero_rest;      // rows of the pairs behind offsets[experts] are set to zero
   uint32_t* counters;     // a tile's arrivals, zero between calls
   uint64_t* partials;     // [tiles][splits] sums of a workgroup's lanes
 };

@@ -27,6 +27,9 @@ namespace tg {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
+// A launch's workgroups are numbered over two dimensions, kGridWidth to a row: one holds fewer than 2^32 threads.
+constexpr int kGridShift = 20, kGridWidth = 1 << kGridShift;
+
 // A workgroup's tile. rows: dense, output rows first .. first + count - 1; experts, places first .. of order.
 struct Tile {
   int ot, rt, sp;             // output tile, row tile, part of the inner axis
@@ -66,7 +69,8 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
   int id;
   {
     const int all = out_tiles * row_tiles * a.splits;
-    const int per = all >> 3, rest = all & 7, x = blockIdx.x & 7, k = blockIdx.x >> 3;
+    const int b = (int)(blockIdx.y << kGridShift | blockIdx.x);
+    const int per = all >> 3, rest = all & 7, x = b & 7, k = b >> 3;
     if (k >= per + (x < rest ? 1 : 0)) return t;
     id = x * per + min(x, rest) + k;
   }
@@ -476,8 +480,9 @@ template <class S, int DT>
 static hipError_t launch_shape_t(const Int8Args& a, hipStream_t s) {
   const int ot = (a.m + S::TO - 1) / S::TO, rt = row_tiles(a, S::TX);
   const int64_t groups = (int64_t)ot * rt * a.splits;
-  if (groups * 64 * S::NW >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;   // more than a launch holds
-  hipLaunchKernelGGL((int8_tile_kernel<S, DT>), dim3((unsigned)groups), dim3(64 * S::NW), 0, s, a, ot, rt);
+  if (groups >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;   // no accepted shape has as many
+  const dim3 grid((unsigned)(groups < kGridWidth ? groups : kGridWidth), (unsigned)((groups + kGridWidth - 1) / kGridWidth));
+  hipLaunchKernelGGL((int8_tile_kernel<S, DT>), grid, dim3(64 * S::NW), 0, s, a, ot, rt);
   return hipGetLastError();
 }
 

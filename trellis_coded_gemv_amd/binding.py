@@ -410,7 +410,8 @@ def trellis_moe_block(gate_up: "LayerTable", down: "LayerTable", sel, weights, x
 # `stream`, or on that device's current stream. Small calls take a few microseconds on the GPU, so
 # the common way through (no stream named, the tensors on the current device) is kept short; any
 # other call enters its device and stream and comes back on the common way, and what it allocates
-# belongs to that stream.
+# belongs to that stream. The C entry points take sizes of 32 bits and ctypes would cut larger ones to
+# their low half, so those (and negative ones) are refused here.
 
 _DTYPES = {}
 
@@ -473,6 +474,8 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int
     if logits.dim() != 2:
         raise ValueError(f"{w}: expected logits [tokens, experts]")
     tokens, experts = logits.shape
+    if (tokens | experts | top_k | n_group | topk_group | group_top) >> 31:
+        raise TgError(-2 if (tokens | experts) >> 31 else -8, w)
     ld, inner = logits.stride()
     if inner != 1 and experts != 1:
         raise ValueError(f"{w}: a token's logits have to be neighbours")
@@ -507,6 +510,8 @@ def moe_group(sel, experts: int, offsets=None, order=None, stream=None):
     if sel.dtype != torch.int32 or not sel.is_contiguous():
         raise ValueError(f"{w}: expected contiguous int32 ids")
     pairs = sel.numel()
+    if (pairs | experts) >> 31:
+        raise TgError(-2, w)
     at = _common_device(w, sel, offsets, order)
     if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
@@ -534,6 +539,8 @@ def int8_quantize(x, q=None, scales=None, stream=None):
     shape = x.shape
     if len(shape) < 1 or x.numel() == 0:
         raise ValueError(f"{w}: expected rows [..., n]")
+    if (x.numel() // shape[-1] | shape[-1]) >> 31:
+        raise TgError(-2, w)
     at = _common_device(w, x, q, scales)
     if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
@@ -607,6 +614,8 @@ class Int8Experts:
 def int8_workspace(layer: "Int8Layer", M: int):
     """Zero-filled workspace for int8_gemm with M rows of this layer."""
     torch = _torch()
+    if (int(M) | layer.m | layer.n) >> 31:
+        raise TgError(-2, "tg_int8_workspace_size")
     size = int(lib().tg_int8_workspace_size(int(M), layer.m, layer.n))
     if size == 0:
         raise TgError(-2, "tg_int8_workspace_size")
@@ -643,6 +652,8 @@ def int8_gemm(layer: "Int8Layer", xq, xs, Y=None, out_dtype=None, ws=None, strea
     w = "int8_gemm"
     m, n = layer.m, layer.n
     M, ldx = _int8_rows(torch, w, n, xq, xs)
+    if (M | m | n) >> 31:
+        raise TgError(-2, w)
     at = _common_device(w, xq, xs, layer.q, Y, ws)
     if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
@@ -668,6 +679,8 @@ def int8_gemm_grouped(experts: "Int8Experts", xq, xs, offsets, order, pairs_per_
     m, n, count = experts.m, experts.n, experts.experts
     rows, ldx = _int8_rows(torch, w, n, xq, xs)
     pairs = rows * int(pairs_per_row)
+    if (pairs | count | m | n) >> 31:
+        raise TgError(-2, w)
     if order.dtype != torch.int32 or order.shape != (pairs,) or not order.is_contiguous():
         raise ValueError(f"{w}: expected order int32 [{pairs}]")
     if offsets.dtype != torch.int32 or offsets.shape != (count + 1,) or not offsets.is_contiguous():

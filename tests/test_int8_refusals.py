@@ -44,3 +44,18 @@ def test_sizes_beyond_32_bits():
         with pytest.raises(tg.TgError):
             call()
             pytest.fail(str(i))
+
+
+def test_stream_of_another_device():
+    """A stream of another GPU than the tensors' is refused; it is not replaced by the tensors' own current stream."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream = 0x5000
+
+        def __init__(self, index):
+            self.device = torch.device("cuda", index)
+    with pytest.raises(ValueError, match="stream"):
+        tg._Entered(0, Stream(1))
+    tg._Entered(1, Stream(1))
+    tg._Entered(0, None)

@@ -452,6 +452,8 @@ class _Entered:
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", at))
+            if stream.device.index != at:
+                raise ValueError(f"a stream of {stream.device} for tensors on cuda:{at}")
             self._enter.append(torch.cuda.stream(stream))
 
     def __enter__(self):

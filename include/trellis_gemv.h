@@ -494,7 +494,8 @@ int32_t moe_route(int32_t tokens, int32_t experts, int32_t top_k, const void *lo
  * whose id lies outside [0, experts); expert e's are order[offsets[e] .. offsets[e + 1] - 1].
  *   pairs   : 1 .. 2^24; experts : 1 .. 1024.
  *   sel     : device, pairs int32.
- *   offsets : device, experts + 1 int32 out; order : device, pairs int32 out.
+ *   offsets : device, experts + 1 int32 out; order : device, pairs int32 out. The three do not overlap
+ *             (TG_ERR_ARG).
  */
 int32_t moe_group(int32_t pairs, int32_t experts, const int32_t *sel, int32_t *offsets, int32_t *order, void *stream);
 

@@ -59,3 +59,15 @@ def test_stream_of_another_device():
         tg._Entered(0, Stream(1))
     tg._Entered(1, Stream(1))
     tg._Entered(0, None)
+
+
+A = 0x100000            # a device address: never dereferenced
+
+
+@pytest.mark.parametrize("sel,offsets,order", [(A, A + 0x10000, A), (A, A + 0x10000, A + 396), (A + 396, A + 0x10000, A), (A, A, A + 0x10000),
+                                               (A, A + 396, A + 0x10000), (A + 32, A, A + 0x10000), (A + 0x10000, A, A), (A + 0x10000, A + 396, A),
+                                               (A + 0x10000, A, A + 32)])
+def test_group_in_place(sel, offsets, order):
+    """The ids are read by every workgroup, twice where they are many, while others write: a place found from ids that have changed
+    meanwhile can lie behind the list. 100 pairs of 8 experts: 400 bytes of ids and of order, 36 of offsets."""
+    assert tg.lib().moe_group(100, 8, sel, offsets, order, None) == -8

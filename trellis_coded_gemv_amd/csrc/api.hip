@@ -737,6 +737,11 @@ namespace {
 
 bool bad_type(int32_t dtype) { return dtype < TG_F32 || dtype > TG_BF16; }
 
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t p = (uintptr_t)a, q = (uintptr_t)b;
+  return p < q + b_bytes && q < p + a_bytes;
+}
+
 size_t type_size(int32_t dtype) { return dtype == TG_F32 ? 4 : 2; }
 
 // 128 * 128 * n < 2^31: no sum of 8-bit products leaves int32.
@@ -805,6 +810,9 @@ TG_API int32_t moe_group(int32_t pairs, int32_t experts, const int32_t* sel, int
   if (pairs < 1 || pairs > (1 << 24) || experts < 1 || experts > kRouteMaxExperts) return TG_ERR_SHAPE;
   if (!sel || !offsets || !order) return TG_ERR_NULL;
   if (misaligned(sel, 4) || misaligned(offsets, 4) || misaligned(order, 4)) return TG_ERR_ALIGN;
+  // Workgroups write while others still read ids: in place, a list that is read twice could be written past its end.
+  const size_t list = 4 * (size_t)pairs, ends = 4 * ((size_t)experts + 1);
+  if (overlap(sel, list, order, list) || overlap(sel, list, offsets, ends) || overlap(order, list, offsets, ends)) return TG_ERR_ARG;
   return launch_status(launch_moe_group(pairs, experts, sel, offsets, order, (hipStream_t)stream));
 }
 

@@ -557,6 +557,14 @@ int32_t int8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int32_t n, 
                           const int32_t *offsets, const int32_t *order, void *Y, int32_t out_dtype, int64_t ldy,
                           void *stream);
 
+/*
+ * The kernel that a product of this shape takes (test and measurement hook; nothing is launched).
+ *   rows    : int8_gemm's M, or int8_gemm_grouped's pairs; experts : 0 for int8_gemm.
+ *   plan    : host, 4 int32 out: the tile shape's number, the parts of the inner axis, the tile's outputs
+ *             and its rows.
+ */
+int32_t tg_int8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_t *plan);
+
 #ifdef __cplusplus
 }
 #endif

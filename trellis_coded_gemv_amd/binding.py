@@ -32,7 +32,8 @@ EXPORTS = ("tg_abi_version", "tg_build_id", "tg_workspace_status", "tg_status_st
            "rht_apply", "trellis_gemv_grouped", "tg_grouped_workspace_size", "trellis_decode", "tg_code_table",
            "trellis_encode", "tg_encode_workspace_size", "trellis_gemm_prefill", "tg_prefill_workspace_size",
            "trellis_moe_block", "tg_moe_workspace_size",
-           "moe_route", "moe_group", "int8_quantize", "int8_gemm", "tg_int8_workspace_size", "int8_gemm_grouped")
+           "moe_route", "moe_group", "int8_quantize", "int8_gemm", "tg_int8_workspace_size", "int8_gemm_grouped",
+           "tg_int8_plan")
 
 TG_ROUTE_SIGMOID = 1
 TG_ROUTE_RENORM = 2
@@ -103,6 +104,7 @@ def lib() -> ctypes.CDLL:
         "int8_quantize": (I32, [I32, I32, P, I32, I64, P, I64, P, P]),
         "int8_gemm": (I32, [I32, I32, I32, P, I64, P, P, I64, P, P, I32, I64, P, SZ, P]),
         "tg_int8_workspace_size": (SZ, [I32, I32, I32]),
+        "tg_int8_plan": (I32, [I32, I32, I32, I32, ctypes.POINTER(I32)]),
         "int8_gemm_grouped": (I32, [I32, I32, I32, I32, P, I64, P, I32, P, P, P, P, P, I32, I64, P]),
     }
     for name, (res, args) in sig.items():

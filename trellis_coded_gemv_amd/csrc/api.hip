@@ -829,6 +829,18 @@ TG_API size_t tg_int8_workspace_size(int32_t M, int32_t m, int32_t n) {
   return check_int8_shape(M, m, n) == TG_OK ? int8_ws_bytes(M, m, n) : 0;
 }
 
+TG_API int32_t tg_int8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_t* plan) {
+  const int32_t st = check_int8_shape(rows, m, n);
+  if (st != TG_OK) return st;
+  if (experts < 0 || experts > kRouteMaxExperts) return TG_ERR_SHAPE;
+  if (!plan) return TG_ERR_NULL;
+  const Int8Plan p = int8_plan(rows, m, n, experts);
+  plan[0] = p.shape;
+  plan[1] = p.splits;
+  int8_plan_tile(p, plan + 2, plan + 3);
+  return TG_OK;
+}
+
 TG_API int32_t int8_gemm(int32_t M, int32_t m, int32_t n, const int8_t* xq, int64_t ldx, const float* xs,
                          const int8_t* wq, int64_t ldw, const float* wscales, void* Y, int32_t out_dtype, int64_t ldy,
                          void* ws, size_t ws_bytes, void* stream) {

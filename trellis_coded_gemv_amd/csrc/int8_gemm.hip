@@ -20,6 +20,7 @@
 // steps of BK bytes, and the operands are read from there.
 #include <type_traits>
 
+#include "int8_tiles.hpp"
 #include "tg_device.hpp"
 #include "tg_internal.hpp"
 
@@ -27,21 +28,17 @@ namespace tg {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
-// A launch's workgroups are numbered over two dimensions, kGridWidth to a row: one holds fewer than 2^32 threads.
-constexpr int kGridShift = 20, kGridWidth = 1 << kGridShift;
-
 // A workgroup's tile. rows: dense, output rows first .. first + count - 1; experts, places first .. of order.
 struct Tile {
   int ot, rt, sp;             // output tile, row tile, part of the inner axis
   int expert, first, count;   // expert -1: rows to set to zero; count 0: nothing to do
 };
 
-// Workgroup -> tile. Workgroups b, b + 8, ... share an XCD and its L2: each XCD takes a run of neighbouring tiles out of
-// those that there are, the same number for each. Dense: 8 row tiles by all output tiles, rows first, so that an XCD's
-// resident workgroups share a few row tiles and output tiles. Experts: the row tiles are numbered expert by expert (every
-// wave finds them from the offsets, up to 16 neighbouring experts to a lane), outputs first, so that an expert's tiles
-// stay together; behind them, where they are to be set to zero, the pairs without an expert; the launch holds the most
-// tiles that the pairs could need, and what is over ends at once.
+// Workgroup -> tile. Dense: 8 row tiles by all output tiles, rows first, so that an XCD's resident workgroups share a few
+// row tiles and output tiles. Experts: the row tiles are numbered expert by expert (every wave finds them from the
+// offsets, up to 16 neighbouring experts to a lane), outputs first, so that an expert's tiles stay together; behind them,
+// where they are to be set to zero, the pairs without an expert; the launch holds the most tiles that the pairs could
+// need, and what is over ends at once.
 // Every value is wave-uniform.
 __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int row_tiles, int rows_per_tile) {
   constexpr int kHeld = 4;                      // experts of a lane whose places are kept
@@ -66,30 +63,17 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
     routed = __builtin_amdgcn_readlane(scan, 63);
     row_tiles = min(row_tiles, routed + (a.zero_rest ? tiles(__builtin_amdgcn_readfirstlane(place(a.experts)), a.M) : 0));
   }
-  int id;
-  {
-    const int all = out_tiles * row_tiles * a.splits;
-    const int b = (int)(blockIdx.y << kGridShift | blockIdx.x);
-    const int per = all >> 3, rest = all & 7, x = b & 7, k = b >> 3;
-    if (k >= per + (x < rest ? 1 : 0)) return t;
-    id = x * per + min(x, rest) + k;
-  }
-  if (a.splits > 1) {
-    const int q = id / a.splits;
-    t.sp = id - q * a.splits;
-    id = q;
-  }
+  const int id = tile_number((int)(blockIdx.y << kGridShift | blockIdx.x), out_tiles * row_tiles * a.splits);
+  if (id < 0) return t;
+  const TilePlace at_tile = tile_place(id, out_tiles, row_tiles, a.splits, !a.offsets);
+  t.ot = at_tile.ot;
+  t.rt = at_tile.rt;
+  t.sp = at_tile.sp;
   if (!a.offsets) {
-    const int band = id / (8 * out_tiles), in = id - band * 8 * out_tiles;
-    const int high = min(8, row_tiles - band * 8);
-    t.ot = in / high;
-    t.rt = band * 8 + in - t.ot * high;
     t.first = t.rt * rows_per_tile;
     t.count = min(rows_per_tile, a.M - t.first);
     return t;
   }
-  t.rt = id / out_tiles;
-  t.ot = id - t.rt * out_tiles;
   if (t.rt >= routed) {
     t.expert = -1;
     t.first = __builtin_amdgcn_readfirstlane(place(a.experts)) + (t.rt - routed) * rows_per_tile;
@@ -223,7 +207,7 @@ struct TileShape {
   static_assert(LW * RPI * NW == TO && LX * RPI * NW == TX, "every wave loads whole instructions");
   // A row's 16-byte pieces are held in LDS in an order that depends on the row, so that the lanes which read the same
   // piece of neighbouring rows spread over the banks.
-  static __device__ __forceinline__ int output(int t, int g) { return AT == 1 ? 4 * g : 32 * (t / 2) + 8 * g + 4 * (t % 2); }
+  static __device__ __forceinline__ int output(int t, int g) { return lane_output(AT, t, g); }
   static __device__ __forceinline__ int swizzle(int row) { return BK >= 128 ? row & 7 : (row >> 1) & 3; }
 };
 
@@ -250,9 +234,7 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
   const int wo = wave % S::WO, wx = wave / S::WO;
 
   // Loads: an instruction fills RPI rows of LDS; lane l the slot l % (BK / 16) of row l / (BK / 16), where the piece
-  // slot ^ swizzle(row) of the row belongs. LDS row 16 (AT wo + t) + 4 g + v of the layer's side holds output
-  // 16 AT wo + 32 (t / 2) + 8 g + 4 (t % 2) + v (one tile to a wave: its row's number), so that a lane ends with 8
-  // neighbouring outputs of a row and the four lanes of the row with 32.
+  // slot ^ swizzle(row) of the row belongs.
   const int lrow = lane / (BK / 16);
   auto wrow = [&](int i) { return S::RPI * (S::LW * wave + i) + lrow; };   // LDS row of this lane in instruction i
   auto xrow = [&](int i) { return S::RPI * (S::LX * wave + i) + lrow; };
@@ -264,7 +246,7 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
 #pragma unroll
   for (int i = 0; i < S::LW; ++i) {
     const int q = wrow(i);
-    const int o = AT == 1 ? q : q / (16 * AT) * (16 * AT) + S::output((q >> 4) % AT, (q >> 2) & 3) + (q & 3);
+    const int o = lds_row_output(AT, q);
     woff[i] = (uint32_t)min(o, a.m - 1 - o0) * (uint32_t)a.ldw;
   }
 #pragma unroll
@@ -548,6 +530,11 @@ Int8Plan int8_plan(int M, int m, int n, int experts) {
     }
   }
   return best;
+}
+
+void int8_plan_tile(const Int8Plan& p, int* outputs, int* rows) {
+  *outputs = kTiles[p.shape].out;
+  *rows = kTiles[p.shape].rows;
 }
 
 size_t int8_partial_bytes(int M, int m, int n) {

@@ -171,6 +171,7 @@ struct Int8Plan {
   int splits;
 };
 Int8Plan int8_plan(int M, int m, int n, int experts);   // experts 0: a dense product
+void int8_plan_tile(const Int8Plan& p, int* outputs, int* rows);
 constexpr int kInt8Counters = 1024;
 constexpr size_t kInt8Partials = kWsHeader + 4 * kInt8Counters;   // offset in the workspace
 size_t int8_partial_bytes(int M, int m, int n);

@@ -1,4 +1,6 @@
-"""The library's own rule and tile numbering: the rule against its model in Python, the numbering compiled for the host."""
+"""The library's own rule and tile numbering: the rule against its model in Python, the numbering compiled for the host, and the
+products that the GPU tests run against what the rule takes."""
+import collections
 import ctypes
 import math
 import os
@@ -8,7 +10,7 @@ import subprocess
 
 import pytest
 
-from int8_shapes import plan
+from int8_shapes import DENSE, GROUPED, plan
 from test_int8_plan_model import plan as model
 from test_int8_plan_model import shapes
 from trellis_coded_gemv_amd import binding as tg
@@ -45,6 +47,15 @@ def test_workspace_holds_the_parts():
         assert tg.lib().tg_int8_workspace_size(M, m, n) >= 256 + 4096 + need
         if parts > 1:
             assert -(-m // outputs) * -(-M // rows) <= 1024          # a counter for each tile
+
+
+def test_the_lists_take_every_kernel():
+    """What the rule takes in one of 5000 products or more, the GPU tests run: tile shapes and parts of dense products, shapes of experts'."""
+    taken = collections.Counter(("experts" if c[3] else "dense",) + plan(*c)[:2] for c in _sweep(40000, 3))
+    often = {k for k, v in taken.items() if v >= 8}
+    run = {("dense",) + plan(*c)[:2] for c in DENSE} | {("experts",) + plan(*c[:4])[:2] for c in GROUPED}
+    assert often <= run, sorted(often - run)
+    assert {k[1] for k in run if k[0] == "dense"} == {k[1] for k in run if k[0] == "experts"} == set(range(len(shapes()[0])))
 
 
 @pytest.fixture(scope="module")

@@ -449,7 +449,9 @@ int32_t trellis_encode(int32_t n_tiles, int32_t k_bits, int32_t code_id, float s
 /* Workspace bytes for trellis_encode (0 if the arguments are invalid). */
 size_t tg_encode_workspace_size(int32_t n_tiles, int32_t k_bits, int32_t code_id);
 
-/* Element types of the routing and 8-bit entry points. */
+/* Routing and 8-bit entry points: outputs and workspaces overlap neither an input nor one another. moe_group
+ * refuses it; the others do not look for it, and leave wrong values inside their outputs.
+ * Element types: */
 #define TG_F32 0
 #define TG_F16 1
 #define TG_BF16 2
@@ -549,8 +551,10 @@ size_t tg_int8_workspace_size(int32_t M, int32_t m, int32_t n);
  *   xq    : device, pairs / pairs_per_row rows, as for int8_gemm; xs : device, as many fp32.
  *   wq    : device, experts * m contiguous rows of n int8, 16-byte aligned; wscales : device, experts * m fp32.
  *   Y     : device, pairs rows, as for int8_gemm.
- * Offsets are cut to [0, pairs] and entries of order outside [0, pairs) are skipped; a pair listed twice
- * for different experts leaves either's product.
+ * offsets do not fall from one expert to the next and order lists every pair once, as moe_group leaves them.
+ * Of others nothing is read or written out of range: offsets are cut to [0, pairs] and entries of order
+ * outside [0, pairs) are skipped. But products may be missing where offsets fall, and a pair listed twice for
+ * different experts leaves either's product.
  */
 int32_t int8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int32_t n, const int8_t *xq, int64_t ldx,
                           const float *xs, int32_t pairs_per_row, const int8_t *wq, const float *wscales,

@@ -99,3 +99,24 @@ def test_block_over_masked_experts():
         assert torch.equal(out, first)
         assert torch.equal(_block(torch, x, logits, gu, dn, top_k), first)
         torch.cuda.synchronize()
+
+
+def test_offsets_that_fall():
+    """Lists that overlap, as no grouping makes them: whatever products are missing, nothing outside the output is written."""
+    dev = device()
+    import torch
+    say("int8 grouped falling offsets")
+    g = torch.Generator().manual_seed(62)
+    pairs, experts, m, n = 300, 40, 70, 64
+    E = tg.Int8Experts.from_dense(torch.randn(experts, m, n, generator=g).to(dev))
+    q, s = tg.int8_quantize(torch.randn(pairs, n, generator=g).to(dev))
+    order = torch.randperm(pairs, generator=g).to(torch.int32).to(dev)
+    for offsets in ([0, pairs] * 20 + [0], [pairs, 0] * 20 + [pairs], list(range(40, -1, -1)), [pairs] * 41, [-1] * 41):
+        off = torch.tensor(offsets, dtype=torch.int32, device=dev)
+        Y = torch.full((pairs + 2, m + 4), 9.0, device=dev)
+        tg.int8_gemm_grouped(E, q, s, off, order, Y=Y[1:-1, 2:-2])
+        y = tg.int8_gemm_grouped(E, q, s, off, order)
+        torch.cuda.synchronize()
+        assert bool((Y[0] == 9).all()) and bool((Y[-1] == 9).all()) and bool((Y[:, :2] == 9).all()) and bool((Y[:, -2:] == 9).all())
+        if offsets[-1] <= 0 and max(offsets) <= 0:                   # every pair is behind the last expert's
+            assert not bool(y.any())

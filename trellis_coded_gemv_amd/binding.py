@@ -508,7 +508,7 @@ def moe_route(logits, top_k: int, bias=None, sigmoid: bool = False, n_group: int
 
 def moe_group(sel, experts: int, offsets=None, order=None, stream=None):
     """The routed pairs (token * top_k + slot) in expert order: offsets int32 [experts + 1] and order int32 [pairs], of
-    int32 ids of any shape; the pairs whose id is no expert come last, behind offsets[experts]."""
+    int32 ids of any shape; the pairs whose id is no expert come last, behind offsets[experts]. The three do not overlap."""
     torch = _torch()
     w = "moe_group"
     if sel.dtype != torch.int32 or not sel.is_contiguous():
@@ -536,7 +536,8 @@ def moe_group(sel, experts: int, offsets=None, order=None, stream=None):
 
 
 def int8_quantize(x, q=None, scales=None, stream=None):
-    """Rows x [..., n] (fp32, fp16 or bf16) as int8 [..., n] with a scale for each row (fp32 [...]): x is about q * scale."""
+    """Rows x [..., n] (fp32, fp16 or bf16) as int8 [..., n] with a scale for each row (fp32 [...]): x is about q * scale. q and
+    scales do not overlap x."""
     torch = _torch()
     w = "int8_quantize"
     dtype = _dtype_code(x.dtype, w)

@@ -5,13 +5,14 @@
 // work; an output is rounded three times in binary32 (the sum, and its product with either scale) and once more to a
 // 16-bit output type.
 //
-// What bounds it (MI355X, 2.2 GHz under this load): 4096 x 28672 x 8192 runs at 2440-2550 TOP/s, 60-63% of what the matrix
-// cores reach on such values from registers alone (4035 TOP/s; 4900 on zeros: the card's power). The loads to LDS alone
-// take 508 of 789 us with these 256 x 256 tiles, and 722 of 899 with 256 x 128 (373 and 456 where every tile reads the
-// same rows, out of L2); the reads from LDS alone 323. So the way into LDS comes next to the power, and the largest tiles
-// ask least of it. The library's own 8-bit product takes 844 us there. 1 x 28672 x 8192 reads 235 MB in 42 us (5.6 TB/s; a
-// large copy moves 5.1). 8192 tokens over 128 experts, 1536 x 2048, top 8: 269 us; the loads to LDS alone 190, the stores
-// 35-43, the first loads and lookups of short tiles some 40. Workgroups that go on to a next tile and begin its loads
+// What bounds it (MI355X, 2.2 GHz under this load): 4096 x 28672 x 8192 runs at 2430-2540 TOP/s (758-793 us), 60-63% of
+// what the matrix cores reach on such values from registers alone (4035 TOP/s; 4900 on zeros: the card's power). The
+// loads to LDS alone take 508 of 789 us with these 256 x 256 tiles, and 722 of 899 with 256 x 128 (373 and 456 where every
+// tile reads the same rows, out of L2); the reads from LDS alone 323. So the way into LDS comes next to the power, and the
+// largest tiles ask least of it. The library's own 8-bit product takes 844 us there. 1 x 28672 x 8192 reads 235 MB in 42
+// us (5.6 TB/s; a large copy moves 5.1). 8192 tokens over 128 experts, 1536 x 2048, top 8: 269-279 us; the loads to LDS
+// alone 190, the stores 35-43, the first loads and lookups of short tiles some 40; 2048 x 768 with a row for each pair:
+// 207-212 us, of which 268 MB of outputs are half the bytes. Workgroups that go on to a next tile and begin its loads
 // before the stores of the last lose (312 -> 320 us with 256 x 128 tiles: loads wait for the stores before them).
 //
 // v_mfma_i32_16x16x64_i8 with the layer's rows as its A operand and the activation rows as its B operand: lane l

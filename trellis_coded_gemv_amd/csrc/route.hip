@@ -516,11 +516,40 @@ hipError_t launch_moe_route(const RouteArgs& a, int dtype, hipStream_t s) {
 // ---------------------------------------------------------------------------
 constexpr int kGroupBatches = 4;  // batches of 8 * 256 ids whose hits a wave keeps: 16 * 4 * 2048 = 2^17 pairs
 
-// 2 v + this lane's bit of the mask, in one addition with carry.
-__device__ __forceinline__ uint32_t twice_plus(uint32_t v, uint64_t mask) {
-  asm("v_addc_co_u32_e64 %0, vcc, %0, %0, %1" : "+v"(v) : "s"(mask) : "vcc");
-  return v;
+// Four neighbouring ids of a lane: hits doubled four times, each time with whether that id is the workgroup's (NONE: is no
+// expert's, >= mine) as the carry of the addition; COUNT: the wave's ids below `mine` are added to less. In one piece, as a
+// carry is read two wait states after its comparison at the earliest and the compiler does not see into an addition
+// written by hand: here three other instructions or more lie between.
+#define TG_EACH(cmp, to)                                                                                             \
+  cmp " %[" to "0], %[id0], %[mine]\n\t" cmp " %[" to "1], %[id1], %[mine]\n\t"                                         \
+  cmp " %[" to "2], %[id2], %[mine]\n\t" cmp " %[" to "3], %[id3], %[mine]\n\t"
+#define TG_PUSH(is) "v_addc_co_u32_e64 %[hits], vcc, %[hits], %[hits], %[" is "]\n\t"
+#define TG_PUSHES TG_PUSH("is0") TG_PUSH("is1") TG_PUSH("is2") TG_PUSH("is3")
+#define TG_OUT [hits] "+&v"(hits), [is0] "=&s"(is0), [is1] "=&s"(is1), [is2] "=&s"(is2), [is3] "=&s"(is3)
+#define TG_LOW [low0] "=&s"(low0), [low1] "=&s"(low1), [low2] "=&s"(low2), [low3] "=&s"(low3)
+#define TG_IN [id0] "v"(id[0]), [id1] "v"(id[1]), [id2] "v"(id[2]), [id3] "v"(id[3]), [mine] "s"(mine)
+template <bool NONE, bool COUNT>
+__device__ __forceinline__ void look_at_four(const u32x4& id, uint32_t mine, uint32_t& hits, int& less) {
+  uint64_t is0, is1, is2, is3;
+  if constexpr (COUNT) {
+    uint64_t low0, low1, low2, low3;
+    if constexpr (NONE)
+      asm(TG_EACH("v_cmp_ge_u32_e64", "is") TG_EACH("v_cmp_lt_u32_e64", "low") TG_PUSHES : TG_OUT, TG_LOW : TG_IN : "vcc");
+    else
+      asm(TG_EACH("v_cmp_eq_u32_e64", "is") TG_EACH("v_cmp_lt_u32_e64", "low") TG_PUSHES : TG_OUT, TG_LOW : TG_IN : "vcc");
+    less += __popcll(low0) + __popcll(low1) + __popcll(low2) + __popcll(low3);
+  } else if constexpr (NONE) {
+    asm(TG_EACH("v_cmp_ge_u32_e64", "is") TG_PUSHES : TG_OUT : TG_IN : "vcc");
+  } else {
+    asm(TG_EACH("v_cmp_eq_u32_e64", "is") TG_PUSHES : TG_OUT : TG_IN : "vcc");
+  }
 }
+#undef TG_EACH
+#undef TG_PUSH
+#undef TG_PUSHES
+#undef TG_OUT
+#undef TG_LOW
+#undef TG_IN
 
 // The pairs of expert `mine` (NONE: mine == experts, those without one) -> their places, and where they end. KEEP: a
 // wave's batches fit kGroupBatches; else they are looked at again for the writing.
@@ -533,7 +562,7 @@ __device__ __forceinline__ int group_pairs(const int32_t* __restrict__ sel, int 
   const int stretch = wave * steps * 256, begin = stretch + lane * 4;
   // Batch b of this lane: a bit for each of its 32 ids that is the workgroup's; the wave's ids before it are added to less.
   int less = 0;
-  auto look = [&](int b) {
+  auto look = [&](int b, auto count) {
     uint32_t hits = 0;
     if (8 * b + 8 <= steps && stretch + (8 * b + 8) * 256 <= pairs) {
       u32x4 v[8];                                             // eight loads in flight
@@ -541,12 +570,7 @@ __device__ __forceinline__ int group_pairs(const int32_t* __restrict__ sel, int 
       for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const u32x4_any*>(sel + begin + (8 * b + i) * 256);
       // A hit is doubled into its place by the addition that adds it: the first of 32 ends on top.
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          less += __popcll(__ballot(v[i][c] < mine));
-          hits = twice_plus(hits, __ballot(NONE ? v[i][c] >= mine : v[i][c] == mine));
-        }
+      for (int i = 0; i < 8; ++i) look_at_four<NONE, decltype(count)::value>(v[i], mine, hits, less);
       return __brev(hits);
     }
     for (int i = 0; i < 8 && 8 * b + i < steps; ++i) {
@@ -569,11 +593,11 @@ __device__ __forceinline__ int group_pairs(const int32_t* __restrict__ sel, int 
       if (b >= batches) break;
       int next = b;
       asm volatile("" : "+s"(next) : "v"(less));              // one batch's loads at a time: four would not fit the registers
-      kept[b] = look(next);
+      kept[b] = look(next, std::true_type{});
       same += __popc(kept[b]);
     }
   } else {
-    for (int b = 0; b < batches; ++b) same += __popc(look(b));
+    for (int b = 0; b < batches; ++b) same += __popc(look(b, std::true_type{}));
   }
   same = __builtin_amdgcn_readlane(wave_scan(same), 63);
   if (lane == 0) {
@@ -625,7 +649,7 @@ __device__ __forceinline__ int group_pairs(const int32_t* __restrict__ sel, int 
 #pragma unroll
     for (int b = 0; b < kGroupBatches; ++b) write(b, kept[b]);
   } else if (same != 0) {
-    for (int b = 0; b < batches; ++b) write(b, look(b));
+    for (int b = 0; b < batches; ++b) write(b, look(b, std::false_type{}));
   }
   return end;
 }

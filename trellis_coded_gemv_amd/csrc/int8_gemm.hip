@@ -37,9 +37,11 @@ struct Tile {
 
 // Workgroup -> tile. Dense: 8 row tiles by all output tiles, rows first, so that an XCD's resident workgroups share a few
 // row tiles and output tiles. Experts: the row tiles are numbered expert by expert (every wave finds them from the
-// offsets, up to 16 neighbouring experts to a lane), outputs first, so that an expert's tiles stay together; behind them,
-// where they are to be set to zero, the pairs without an expert; the launch holds the most tiles that the pairs could
-// need, and what is over ends at once.
+// offsets, up to 16 neighbouring experts to a lane), outputs first, so that an expert's tiles stay together; the launch
+// holds the most tiles that the pairs could need, and what is over ends at once. Pairs without an expert, where their rows
+// are to be set to zero, are numbered apart and behind them, one by one over the XCDs: in one run with the experts' they
+// fill whole XCDs, which leave the products to the others (8192 tokens over 128 experts, half of the pairs without one: 168
+// us with their rows left, 241 in one run, 193 apart).
 // Every value is wave-uniform.
 __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int row_tiles, int rows_per_tile) {
   constexpr int kHeld = 4;                      // experts of a lane whose places are kept
@@ -47,7 +49,6 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
   const int lane = threadIdx.x & 63;
   const int per_lane = (a.experts + 63) >> 6;
   int at[kHeld + 1], mine = 0, scan = 0;        // where a lane's experts begin, and the one behind them
-  int routed = 0;                               // row tiles of the experts
   // Past the last expert: where it ends, so none of its own. Places are cut to [0, M].
   auto place = [&](int e) { return min(max(a.offsets[min(e, a.experts)], 0), a.M); };
   auto tiles = [&](int from, int to) { return to > from ? (to - from + rows_per_tile - 1) / rows_per_tile : 0; };
@@ -61,23 +62,26 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
       for (int i = 0; i < per_lane; ++i) mine += tiles(place(lane * per_lane + i), place(lane * per_lane + i + 1));
     }
     scan = wave_scan(mine);
-    routed = __builtin_amdgcn_readlane(scan, 63);
-    row_tiles = min(row_tiles, routed + (a.zero_rest ? tiles(__builtin_amdgcn_readfirstlane(place(a.experts)), a.M) : 0));
+    row_tiles = min(row_tiles, __builtin_amdgcn_readlane(scan, 63));
   }
-  const int id = tile_number((int)(blockIdx.y << kGridShift | blockIdx.x), out_tiles * row_tiles * a.splits);
-  if (id < 0) return t;
+  const int b = (int)(blockIdx.y << kGridShift | blockIdx.x), all = out_tiles * row_tiles * a.splits;
+  const int id = tile_number(b, all);
+  if (id < 0) {
+    const int behind = b - ((all + 7) & ~7);
+    if (!a.zero_rest || behind < 0) return t;
+    const int nth = behind / out_tiles;
+    t.ot = behind - nth * out_tiles;
+    t.expert = -1;
+    t.first = __builtin_amdgcn_readfirstlane(place(a.experts)) + nth * rows_per_tile;
+    t.count = min(rows_per_tile, a.M - t.first);
+    return t;
+  }
   const TilePlace at_tile = tile_place(id, out_tiles, row_tiles, a.splits, !a.offsets);
   t.ot = at_tile.ot;
   t.rt = at_tile.rt;
   t.sp = at_tile.sp;
   if (!a.offsets) {
     t.first = t.rt * rows_per_tile;
-    t.count = min(rows_per_tile, a.M - t.first);
-    return t;
-  }
-  if (t.rt >= routed) {
-    t.expert = -1;
-    t.first = __builtin_amdgcn_readfirstlane(place(a.experts)) + (t.rt - routed) * rows_per_tile;
     t.count = min(rows_per_tile, a.M - t.first);
     return t;
   }
@@ -462,7 +466,7 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
 template <class S, int DT>
 static hipError_t launch_shape_t(const Int8Args& a, hipStream_t s) {
   const int ot = (a.m + S::TO - 1) / S::TO, rt = row_tiles(a, S::TX);
-  const int64_t groups = (int64_t)ot * rt * a.splits;
+  const int64_t groups = (int64_t)ot * rt * a.splits + (a.zero_rest ? 8 : 0);   // 8: zeros begin at a multiple of it
   if (groups >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;   // no accepted shape has as many
   const dim3 grid((unsigned)(groups < kGridWidth ? groups : kGridWidth), (unsigned)((groups + kGridWidth - 1) / kGridWidth));
   hipLaunchKernelGGL((int8_tile_kernel<S, DT>), grid, dim3(64 * S::NW), 0, s, a, ot, rt);

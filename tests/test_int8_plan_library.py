@@ -71,6 +71,7 @@ void place(int id, int out_tiles, int row_tiles, int splits, int dense, int* p) 
   const tg::TilePlace t = tg::tile_place(id, out_tiles, row_tiles, splits, dense != 0);
   p[0] = t.ot; p[1] = t.rt; p[2] = t.sp;
 }
+int zeros(int b, int all) { return tg::zeros_number(b, all); }
 int first_output(int tiles, int t, int g) { return tg::lane_output(tiles, t, g); }
 int row_output(int tiles, int q) { return tg::lds_row_output(tiles, q); }
 int grid_width() { return tg::kGridWidth; }
@@ -116,6 +117,27 @@ def test_every_place_is_taken_once(tiles, out_tiles, row_tiles, splits, dense):
     assert len(got) == len(want) and set(got) == want
     for i in range(0, len(got), splits):                             # a tile's parts are neighbours
         assert {g[:2] for g in got[i:i + splits]} == {got[i][:2]}
+
+
+def test_tiles_of_experts_and_of_zeros(tiles):
+    """However the pairs fall, the launch (row tiles that they could need, and 8 workgroups) holds every expert's tiles once and those of
+    the pairs without one once."""
+    rng = random.Random(4)
+    for _ in range(600):
+        pairs, experts, rows, out_tiles = rng.randint(1, 400), rng.randint(1, 30), rng.choice([16, 32, 64, 128, 256]), rng.randint(1, 9)
+        lists = [0] * (experts + 1)
+        for _ in range(pairs):
+            lists[rng.randint(0, experts) if rng.random() < 0.5 else rng.choice([0, experts])] += 1
+        bound = pairs // rows + min(experts + 1, pairs)
+        routed = out_tiles * sum(-(-c // rows) for c in lists[:experts])
+        zeros = out_tiles * -(-lists[experts] // rows)
+        products, cleared = [], []
+        for b in range(out_tiles * bound + 8):
+            if tiles.number(b, routed) >= 0:
+                products.append(tiles.number(b, routed))
+            elif 0 <= tiles.zeros(b, routed) < zeros:
+                cleared.append(tiles.zeros(b, routed))
+        assert sorted(products) == list(range(routed)) and sorted(cleared) == list(range(zeros))
 
 
 @pytest.mark.parametrize("case", range(7))

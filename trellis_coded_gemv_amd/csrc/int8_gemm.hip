@@ -67,7 +67,7 @@ __device__ __forceinline__ Tile find_tile(const Int8Args& a, int out_tiles, int 
   const int b = (int)(blockIdx.y << kGridShift | blockIdx.x), all = out_tiles * row_tiles * a.splits;
   const int id = tile_number(b, all);
   if (id < 0) {
-    const int behind = b - ((all + 7) & ~7);
+    const int behind = zeros_number(b, all);
     if (!a.zero_rest || behind < 0) return t;
     const int nth = behind / out_tiles;
     t.ot = behind - nth * out_tiles;
@@ -466,7 +466,7 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void int8_tile_kernel(const Int
 template <class S, int DT>
 static hipError_t launch_shape_t(const Int8Args& a, hipStream_t s) {
   const int ot = (a.m + S::TO - 1) / S::TO, rt = row_tiles(a, S::TX);
-  const int64_t groups = (int64_t)ot * rt * a.splits + (a.zero_rest ? 8 : 0);   // 8: zeros begin at a multiple of it
+  const int64_t groups = (int64_t)ot * rt * a.splits + (a.zero_rest ? 8 : 0);   // 8: as zeros_number asks
   if (groups >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;   // no accepted shape has as many
   const dim3 grid((unsigned)(groups < kGridWidth ? groups : kGridWidth), (unsigned)((groups + kGridWidth - 1) / kGridWidth));
   hipLaunchKernelGGL((int8_tile_kernel<S, DT>), grid, dim3(64 * S::NW), 0, s, a, ot, rt);

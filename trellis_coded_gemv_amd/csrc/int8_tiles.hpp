@@ -25,6 +25,10 @@ TG_BOTH int tile_number(int b, int all) {
   return x * per + (x < rest ? x : rest) + k;
 }
 
+// Workgroup b -> its number among the tiles of rows to set to zero, which are numbered behind `all` others from a multiple
+// of 8 on and so spread over the XCDs; negative: none. At most 7 workgroups lie between.
+TG_BOTH int zeros_number(int b, int all) { return b - ((all + 7) & ~7); }
+
 // Dense: bands of 8 row tiles, rows first, then outputs. Else row tile by row tile, outputs first.
 TG_BOTH TilePlace tile_place(int id, int out_tiles, int row_tiles, int splits, bool dense) {
   TilePlace t{0, 0, 0};

@@ -756,7 +756,7 @@ int32_t check_int8_shape(int32_t rows, int32_t m, int32_t n) {
 }
 
 // The operands that a dense product and the experts' share, after the shape has been checked.
-int32_t check_int8_operands(const Int8Args& a) {
+int32_t check_int8_operands(const Product8Args& a) {
   if (!a.x || !a.xs || !a.w || !a.ws || !a.y) return TG_ERR_NULL;
   if (bad_type(a.out) || a.ldx < a.n || a.ldx % 16 != 0 || a.ldw < a.n || a.ldw % 16 != 0 || a.ldw > kInt8MaxStride ||
       a.ldy < a.m)
@@ -846,7 +846,7 @@ TG_API int32_t int8_gemm(int32_t M, int32_t m, int32_t n, const int8_t* xq, int6
                          void* ws, size_t ws_bytes, void* stream) {
   int32_t st = check_int8_shape(M, m, n);
   if (st != TG_OK) return st;
-  Int8Args a{};
+  Product8Args a{};
   a.x = xq;
   a.xs = xs;
   a.w = wq;
@@ -878,7 +878,7 @@ TG_API int32_t int8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int3
   if (st != TG_OK) return st;
   if (experts < 1 || experts > kRouteMaxExperts) return TG_ERR_SHAPE;
   if (pairs_per_row < 1 || pairs % pairs_per_row != 0) return TG_ERR_ARG;
-  Int8Args a{};
+  Product8Args a{};
   a.x = xq;
   a.xs = xs;
   a.w = wq;

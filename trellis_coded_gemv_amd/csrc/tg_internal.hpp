@@ -147,8 +147,9 @@ struct RouteArgs {
 hipError_t launch_moe_route(const RouteArgs& a, int dtype, hipStream_t s);
 hipError_t launch_moe_group(int pairs, int experts, const int32_t* sel, int32_t* offsets, int32_t* order, hipStream_t s);
 
-// 8-bit rows (int8_quantize.hip) and products (int8_gemm.hip): dense, or the experts of routed pairs when offsets is set.
-struct Int8Args {
+// 8-bit rows (int8_quantize.hip) and products (int8_gemm.hip, fp8_gemm.hip): dense, or the experts of routed pairs when
+// offsets is set.
+struct Product8Args {
   const int8_t* x;
   const float* xs;
   const int8_t* w;        // [experts][m] rows
@@ -177,7 +178,7 @@ constexpr size_t kInt8Partials = kWsHeader + 4 * kInt8Counters;   // offset in t
 size_t int8_partial_bytes(int M, int m, int n);
 hipError_t launch_int8_quantize(int rows, int n, const void* x, int dtype, int64_t ldx, int8_t* q, int64_t ldq,
                                 float* scales, hipStream_t s);
-hipError_t launch_int8_gemm(const Int8Args& a, hipStream_t s);
+hipError_t launch_int8_gemm(const Product8Args& a, hipStream_t s);
 constexpr int kEncMaxSlots = 256;        // encoder workgroups in flight (one tile each at a time)
 
 // LDS bytes a GEMV workgroup needs for a chunk of `chunk_blocks` 128-blocks.

@@ -569,6 +569,89 @@ int32_t int8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int32_t n, 
  */
 int32_t tg_int8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_t *plan);
 
+/* Outputs of rms_norm beside TG_F32, TG_F16 and TG_BF16. e4m3: sign, four bits of exponent, three of mantissa, up to 448, no
+ * infinity (torch.float8_e4m3fn). */
+#define TG_INT8 3
+#define TG_E4M3 4
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition before it and a quantiser behind it (what stands in front
+ * of every linear layer of a decoder: lecture, Part one):
+ *     h = x + residual, summed in binary32 and rounded to the residual's type (x itself without a residual); h goes to total,
+ *     r = 1 / sqrt(mean_i h_i^2 + eps), the sum in binary64,
+ *     y_i = h_i * w_i * r                                          out_dtype TG_F32, TG_F16, TG_BF16
+ *     amax = max_i |h_i w_i|, q_i = the whole number nearest to 127 h_i w_i / amax (an exact half to the even one),
+ *            scale = amax * r / 127                                out_dtype TG_INT8: what int8_gemm reads
+ *     amax over each 128 neighbours (fewer at the row's end), q_i = the e4m3 value nearest to 448 h_i w_i / amax (ties to the
+ *            even code), scale = amax * r / 448                    out_dtype TG_E4M3: what fp8_gemm reads
+ * The norm scales a row as a whole, so the steps q do not depend on it; they are decided exactly, on exact products h_i w_i.
+ * y and the scales are rounded from binary64. A row of zeros gives zeros. A row with a NaN or an infinity in h gives NaN, in
+ * 8 bits zeros with NaN scales; a NaN or an infinity in w only its own y_i, or the scale of its row or 128 values.
+ *   rows : 1 .. 2^24; n : 1 .. 32768.
+ *   x        : device, rows of n values of type dtype, row stride ldx >= n elements.
+ *   residual : device, rows of n values of type residual_dtype, stride ldr, or NULL; total : as residual, stride ldt; may be
+ *              residual itself (with ldt == ldr) or, of the same type and stride, x.
+ *   weight   : device, n values of type weight_dtype. eps : finite, >= 0.
+ *   y        : device, rows of n values of type out_dtype, row stride ldy >= n elements.
+ *   scales   : device fp32, row stride lds: one for each row (TG_INT8), or one for each 128 values (TG_E4M3); else not used.
+ */
+int32_t rms_norm(int32_t rows, int32_t n, const void *x, int32_t dtype, int64_t ldx, const void *residual,
+                 int32_t residual_dtype, int64_t ldr, void *total, int64_t ldt, const void *weight,
+                 int32_t weight_dtype, float eps, void *y, int32_t out_dtype, int64_t ldy, float *scales,
+                 int64_t lds, void *stream);
+
+/*
+ * e4m3 rows with a scale for each 128 values, or (block_rows 128) an e4m3 layer with a scale for each block of 128 x 128:
+ * amax = the block's largest |x_i|, scale = amax / 448, q_i = the e4m3 value nearest to 448 x_i / amax (ties to the even
+ * code), so x_i is about q_i * scale. The quotient's rounding is decided exactly; scale is rounded once. A block of zeros
+ * gets scale 0 and zeros; a block with a NaN or an infinity gets scale NaN and zeros, so its products are NaN. Blocks at
+ * the end of a row or of the layer hold what is there.
+ *   rows : 1 .. 2^24; n : 1 .. 2^22; rows * n <= 2^38. block_rows : 1 or 128.
+ *   x    : device, rows of n values of type dtype, row stride ldx >= n elements.
+ *   q    : device, rows of n bytes out, row stride ldq >= n (what lies between rows is left as it was).
+ *   scales : device, fp32 out, a row of ceil(n / 128) for each block_rows rows, row stride lds.
+ */
+int32_t fp8_quantize(int32_t rows, int32_t n, const void *x, int32_t dtype, int64_t ldx, int32_t block_rows, uint8_t *q,
+                     int64_t ldq, float *scales, int64_t lds, void *stream);
+
+/*
+ * Matrix product of e4m3 rows and an e4m3 layer with a scale for each block, on the matrix cores:
+ *     Y[r, o] = sum_b xs[r, b] * ws[o / 128, b] * sum_{i in block b} xq[r, i] * wq[o, i],   blocks of 128 along the inner axis.
+ * A block's scaled sum is added in binary32, in rising order of the blocks (parts of a split inner axis in rising order too), so
+ * the same call gives the same bits. A TG_F32 output has sums of binary32 throughout. The sums behind a 16-bit output are the
+ * matrix cores' 8-bit ones, which align eight neighbouring products to the largest of them and drop what lies below 2^-13 of it:
+ * of values whose blocks were scaled by fp8_quantize, about 2^-16 of the result.
+ *   M, m, n : as for int8_gemm.
+ *   xq : device, M rows of n e4m3 values, 16-byte aligned, row stride ldx >= n bytes, a multiple of 16.
+ *   xs : device, M rows of ceil(n / 128) fp32, row stride ldxs.
+ *   wq : device, m rows of n e4m3 values, aligned as xq, ldw <= 2^23.
+ *   wscales : device, ceil(m / 128) contiguous rows of ceil(n / 128) fp32.
+ *   Y  : device, M rows of m values of type out_dtype, row stride ldy >= m elements.
+ *   ws : device workspace, ws_bytes >= tg_fp8_workspace_size(M, m, n), to be treated as int8_gemm's; one buffer may serve both.
+ */
+int32_t fp8_gemm(int32_t M, int32_t m, int32_t n, const uint8_t *xq, int64_t ldx, const float *xs, int64_t ldxs,
+                 const uint8_t *wq, int64_t ldw, const float *wscales, void *Y, int32_t out_dtype, int64_t ldy,
+                 void *ws, size_t ws_bytes, void *stream);
+
+/* Workspace bytes for fp8_gemm (0 if the shape is invalid). */
+size_t tg_fp8_workspace_size(int32_t M, int32_t m, int32_t n);
+
+/*
+ * The experts' products over routed pairs, in one launch: int8_gemm_grouped with e4m3 rows and layers and their scales,
+ *     Y[p, o] = sum_b xs[t, b] * wscales[e, o / 128, b] * sum_{i in block b} xq[t, i] * wq[e, o, i],  t = p / pairs_per_row.
+ * Pairs, experts, offsets, order, unrouted rows and TG_ZERO_UNROUTED are as they are there.
+ *   xq    : device, pairs / pairs_per_row rows, as for fp8_gemm; xs : their scales.
+ *   wq    : device, experts * m contiguous rows of n e4m3 values, 16-byte aligned; wscales : device, for each expert
+ *           ceil(m / 128) contiguous rows of ceil(n / 128) fp32.
+ */
+int32_t fp8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int32_t n, const uint8_t *xq, int64_t ldx,
+                         const float *xs, int64_t ldxs, int32_t pairs_per_row, const uint8_t *wq, const float *wscales,
+                         const int32_t *offsets, const int32_t *order, void *Y, int32_t out_dtype, int64_t ldy,
+                         void *stream);
+
+/* The kernel that an e4m3 product of this shape takes, as tg_int8_plan. */
+int32_t tg_fp8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_t *plan);
+
 #ifdef __cplusplus
 }
 #endif

@@ -33,7 +33,8 @@ EXPORTS = ("tg_abi_version", "tg_build_id", "tg_workspace_status", "tg_status_st
            "trellis_encode", "tg_encode_workspace_size", "trellis_gemm_prefill", "tg_prefill_workspace_size",
            "trellis_moe_block", "tg_moe_workspace_size",
            "moe_route", "moe_group", "int8_quantize", "int8_gemm", "tg_int8_workspace_size", "int8_gemm_grouped",
-           "tg_int8_plan")
+           "tg_int8_plan",
+           "rms_norm", "fp8_quantize", "fp8_gemm", "tg_fp8_workspace_size", "fp8_gemm_grouped", "tg_fp8_plan")
 
 TG_ROUTE_SIGMOID = 1
 TG_ROUTE_RENORM = 2
@@ -106,6 +107,12 @@ def lib() -> ctypes.CDLL:
         "tg_int8_workspace_size": (SZ, [I32, I32, I32]),
         "tg_int8_plan": (I32, [I32, I32, I32, I32, ctypes.POINTER(I32)]),
         "int8_gemm_grouped": (I32, [I32, I32, I32, I32, P, I64, P, I32, P, P, P, P, P, I32, I64, P]),
+        "rms_norm": (I32, [I32, I32, P, I32, I64, P, I32, I64, P, I64, P, I32, ctypes.c_float, P, I32, I64, P, I64, P]),
+        "fp8_quantize": (I32, [I32, I32, P, I32, I64, I32, P, I64, P, I64, P]),
+        "fp8_gemm": (I32, [I32, I32, I32, P, I64, P, I64, P, I64, P, P, I32, I64, P, SZ, P]),
+        "tg_fp8_workspace_size": (SZ, [I32, I32, I32]),
+        "fp8_gemm_grouped": (I32, [I32, I32, I32, I32, P, I64, P, I64, I32, P, P, P, P, P, I32, I64, P]),
+        "tg_fp8_plan": (I32, [I32, I32, I32, I32, ctypes.POINTER(I32)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -732,6 +739,281 @@ class Int8Linear:
                 self._earlier.append(self._ws)
                 self._ws = ws
         return int8_gemm(self.layer, xq, xs, ws=ws).reshape(x.shape[:-1] + (m,))
+
+    __call__ = forward
+
+
+# ---- norm and e4m3 products ----------------------------------------------------------------
+
+_FP8_BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return (n + _FP8_BLOCK - 1) // _FP8_BLOCK
+
+
+def _rows_of(x):
+    """x [..., n] as rows with neighbouring values: (rows, n, the tensor that holds them, their stride)."""
+    n = x.shape[-1]
+    x2 = x if x.dim() == 2 else x.reshape(-1, n)
+    if x2.stride(1) != 1 and n > 1:
+        x2 = x2.contiguous()
+    rows = x2.shape[0]
+    return rows, n, x2, (x2.stride(0) if rows > 1 else n)
+
+
+def _rows_out(where: str, name: str, t, shape, dtype, device):
+    """A caller's output, checked, or a new one: (tensor, row stride)."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=device), shape[-1]
+    _expect(t.dtype == dtype and t.shape == shape, where, f"expected {name} {dtype} {tuple(shape)}")
+    _expect(t.is_contiguous() or (t.dim() == 2 and (t.stride(1) == 1 or shape[1] == 1) and (t.stride(0) >= shape[1] or shape[0] == 1)), where,
+            f"expected {name} with neighbouring values")
+    return t, (t.stride(0) if t.dim() == 2 and shape[0] > 1 else shape[-1])
+
+
+def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, total=None, y=None, scales=None, stream=None):
+    """Root-mean-square norm of the rows of x [..., n] (fp32, fp16 or bf16), times weight [n], with the residual's addition
+    before it. out_dtype float32, float16 or bfloat16 (x's own by default): y [..., n]. int8: (q [..., n], scales [...]), what
+    int8_gemm reads. float8_e4m3fn: (q [..., n], scales [..., ceil(n / 128)]), what fp8_gemm reads. With a residual [..., n], x +
+    residual, rounded to the residual's type, is what is normed, and comes back as one more output, total; total=residual adds
+    in place. Other outputs overlap neither an input nor one another."""
+    torch = _torch()
+    w = "rms_norm"
+    dtype = _dtype_code(x.dtype, w)
+    out_dtype = out_dtype or (x.dtype if y is None else y.dtype)
+    out = {torch.int8: 3, torch.float8_e4m3fn: 4}.get(out_dtype)
+    if out is None:
+        out = _dtype_code(out_dtype, w)
+    shape = x.shape
+    if len(shape) < 1 or x.numel() == 0:
+        raise ValueError(f"{w}: expected rows [..., n]")
+    if (x.numel() // shape[-1] | shape[-1]) >> 31:
+        raise TgError(-2, w)
+    _expect(weight.shape == shape[-1:] and weight.is_contiguous(), w, f"expected a contiguous weight [{shape[-1]}]")
+    wtype = _dtype_code(weight.dtype, w)
+    rtype = 0
+    if residual is not None:
+        rtype = _dtype_code(residual.dtype, w)
+        _expect(residual.shape == shape, w, f"expected a residual {tuple(shape)}")
+    else:
+        _expect(total is None, w, "total without a residual")
+    at = _common_device(w, x, weight, residual, total, y, scales)
+    if stream is not None or at != torch._C._cuda_getDevice():
+        with _Entered(at, stream):
+            return rms_norm(x, weight, residual, eps, out_dtype, total, y, scales)
+    rows, n, x2, ldx = _rows_of(x)
+    r2, ldr, ldt = None, n, n
+    if residual is not None:
+        _, _, r2, ldr = _rows_of(residual)
+        total, ldt = _rows_out(w, "total", total, shape, residual.dtype, x.device)
+    y, ldy = _rows_out(w, "y", y, shape, out_dtype, x.device)
+    lds = 0
+    if out == 4:
+        scales, lds = _rows_out(w, "scales", scales, shape[:-1] + (_blocks(n),), torch.float32, x.device)
+    elif out == 3:
+        scales, lds = _row_scales(w, scales, shape[:-1], x.device), 1
+    else:
+        _expect(scales is None, w, "scales without 8-bit outputs")
+    status = (_lib or lib()).rms_norm(rows, n, x2.data_ptr(), dtype, ldx, None if r2 is None else r2.data_ptr(), rtype, ldr,
+                                      None if total is None else total.data_ptr(), ldt, weight.data_ptr(), wtype, eps, y.data_ptr(), out, ldy,
+                                      None if scales is None else scales.data_ptr(), lds, torch._C._cuda_getCurrentRawStream(at))
+    if status:
+        raise TgError(status, w)
+    got = (y,) if out < 3 else (y, scales)
+    if residual is not None:
+        got += (total,)
+    return got if len(got) > 1 else y
+
+
+def _row_scales(where: str, scales, lead, device):
+    if scales is None:
+        return _torch().empty(lead, dtype=_torch().float32, device=device)
+    _expect(scales.dtype == _torch().float32 and scales.shape == lead and scales.is_contiguous(), where, "expected a float32 scale for each row")
+    return scales
+
+
+def fp8_quantize(x, q=None, scales=None, block_rows: int = 1, stream=None):
+    """Rows x [..., n] (fp32, fp16 or bf16) as e4m3 [..., n] (float8_e4m3fn) with a scale for each 128 values (fp32 [..., ceil(n / 128)]):
+    x is about q * scale. block_rows=128: x [m, n] with a scale for each block of 128 x 128 (fp32 [ceil(m / 128), ceil(n / 128)]),
+    a layer. q and scales do not overlap x."""
+    torch = _torch()
+    w = "fp8_quantize"
+    dtype = _dtype_code(x.dtype, w)
+    shape = x.shape
+    if len(shape) < 1 or x.numel() == 0:
+        raise ValueError(f"{w}: expected rows [..., n]")
+    _expect(block_rows == 1 or (block_rows == _FP8_BLOCK and len(shape) == 2), w, "block_rows is 1, or 128 of x [m, n]")
+    if (x.numel() // shape[-1] | shape[-1]) >> 31:
+        raise TgError(-2, w)
+    at = _common_device(w, x, q, scales)
+    if stream is not None or at != torch._C._cuda_getDevice():
+        with _Entered(at, stream):
+            return fp8_quantize(x, q, scales, block_rows)
+    rows, n, x2, ldx = _rows_of(x)
+    q, ldq = _rows_out(w, "q", q, shape, torch.float8_e4m3fn, x.device)
+    lead = shape[:-1] if block_rows == 1 else (_blocks(rows),)
+    scales, lds = _rows_out(w, "scales", scales, lead + (_blocks(n),), torch.float32, x.device)
+    status = (_lib or lib()).fp8_quantize(rows, n, x2.data_ptr(), dtype, ldx, block_rows, q.data_ptr(), ldq, scales.data_ptr(), lds,
+                                          torch._C._cuda_getCurrentRawStream(at))
+    if status:
+        raise TgError(status, w)
+    return q, scales
+
+
+class Fp8Layer:
+    """A linear layer kept in e4m3: q float8_e4m3fn [m, n] with a scale for each block of 128 x 128 (fp32 [ceil(m / 128), ceil(n / 128)])."""
+
+    def __init__(self, q, scales):
+        torch = _torch()
+        w = "Fp8Layer"
+        _expect(q.dtype == torch.float8_e4m3fn and q.dim() == 2 and q.stride(1) == 1, w, "expected q float8_e4m3fn [m, n] with neighbouring inputs")
+        want = (_blocks(q.shape[0]), _blocks(q.shape[1]))
+        _expect(scales.dtype == torch.float32 and scales.shape == want and scales.is_contiguous(), w, f"expected contiguous float32 scales {want}")
+        _common_device(w, q, scales)
+        self.q, self.scales, self.device = q, scales, q.device
+        self.m, self.n = int(q.shape[0]), int(q.shape[1])
+        self.ldw = q.stride(0) if self.m > 1 else self.n
+
+    @classmethod
+    def from_dense(cls, weight, stream=None):
+        """The nearest e4m3 layer of a dense weight [m, n] (fp32, fp16 or bf16)."""
+        return cls(*fp8_quantize(weight, block_rows=_FP8_BLOCK, stream=stream))
+
+
+class Fp8Experts:
+    """The experts of a block, kept in e4m3: q float8_e4m3fn [experts, m, n], scales fp32 [experts, ceil(m / 128), ceil(n / 128)]."""
+
+    def __init__(self, q, scales):
+        torch = _torch()
+        w = "Fp8Experts"
+        _expect(q.dtype == torch.float8_e4m3fn and q.dim() == 3 and q.is_contiguous(), w, "expected contiguous q float8_e4m3fn [experts, m, n]")
+        want = (q.shape[0], _blocks(q.shape[1]), _blocks(q.shape[2]))
+        _expect(scales.dtype == torch.float32 and scales.shape == want and scales.is_contiguous(), w, f"expected contiguous float32 scales {want}")
+        _common_device(w, q, scales)
+        self.q, self.scales, self.device = q, scales, q.device
+        self.experts, self.m, self.n = (int(v) for v in q.shape)
+
+    @classmethod
+    def from_dense(cls, weight, stream=None):
+        """The nearest e4m3 experts of dense weights [experts, m, n]."""
+        torch = _torch()
+        _expect(weight.dim() == 3, "Fp8Experts", "expected weights [experts, m, n]")
+        experts, m, n = weight.shape
+        q = torch.empty(experts, m, n, dtype=torch.float8_e4m3fn, device=weight.device)
+        scales = torch.empty(experts, _blocks(m), _blocks(n), dtype=torch.float32, device=weight.device)
+        for e in range(experts):
+            fp8_quantize(weight[e], q[e], scales[e], _FP8_BLOCK, stream)
+        return cls(q, scales)
+
+
+def fp8_workspace(layer: "Fp8Layer", M: int):
+    """Zero-filled workspace for fp8_gemm with M rows of this layer."""
+    torch = _torch()
+    if (int(M) | layer.m | layer.n) >> 31:
+        raise TgError(-2, "tg_fp8_workspace_size")
+    size = int(lib().tg_fp8_workspace_size(int(M), layer.m, layer.n))
+    if size == 0:
+        raise TgError(-2, "tg_fp8_workspace_size")
+    return torch.zeros(size, dtype=torch.uint8, device=layer.device)
+
+
+def _fp8_rows(torch, where: str, n: int, xq, xs):
+    if xq.dtype != torch.float8_e4m3fn or xq.dim() != 2:
+        raise ValueError(f"{where}: expected xq float8_e4m3fn [rows, {n}]")
+    rows, width = xq.shape
+    ldx, inner = xq.stride()
+    if width != n or inner != 1:
+        raise ValueError(f"{where}: expected xq float8_e4m3fn [rows, {n}] with neighbouring values")
+    blocks = _blocks(n)
+    if xs.dtype != torch.float32 or xs.shape != (rows, blocks) or (xs.stride(1) != 1 and blocks > 1):
+        raise ValueError(f"{where}: expected float32 scales [rows, {blocks}] of xq, a row's neighbouring")
+    return rows, (ldx if rows > 1 else n), (xs.stride(0) if rows > 1 else blocks)
+
+
+def fp8_gemm(layer: "Fp8Layer", xq, xs, Y=None, out_dtype=None, ws=None, stream=None):
+    """Y [M, m] = sum over blocks b of 128 inputs of (xq_b wq_b^T) * xs[r, b] * scales[o // 128, b], of e4m3 rows xq [M, n] with scales
+    xs [M, ceil(n / 128)]; out_dtype (or Y's type) float32, float16 or bfloat16."""
+    torch = _torch()
+    w = "fp8_gemm"
+    m, n = layer.m, layer.n
+    M, ldx, ldxs = _fp8_rows(torch, w, n, xq, xs)
+    if (M | m | n) >> 31:
+        raise TgError(-2, w)
+    at = _common_device(w, xq, xs, layer.q, Y, ws)
+    if stream is not None or at != torch._C._cuda_getDevice():
+        with _Entered(at, stream):
+            return fp8_gemm(layer, xq, xs, Y, out_dtype, ws)
+    Y, code, ldy = _int8_out(torch, w, Y, M, m, out_dtype, xq)
+    if ws is None:
+        ws = fp8_workspace(layer, M)
+    elif not ws.is_contiguous():
+        raise ValueError(f"{w}: expected a contiguous workspace")
+    status = (_lib or lib()).fp8_gemm(M, m, n, xq.data_ptr(), ldx, xs.data_ptr(), ldxs, layer.q.data_ptr(), layer.ldw, layer.scales.data_ptr(),
+                                      Y.data_ptr(), code, ldy, ws.data_ptr(), ws.numel() * ws.element_size(), torch._C._cuda_getCurrentRawStream(at))
+    if status:
+        raise TgError(status, w)
+    return Y
+
+
+def fp8_gemm_grouped(experts: "Fp8Experts", xq, xs, offsets, order, pairs_per_row: int = 1, Y=None, out_dtype=None, stream=None):
+    """Y [pairs, m]: row p = order[j], offsets[e] <= j < offsets[e + 1], is expert e's product with the e4m3 row
+    xq[p // pairs_per_row] and its scales. Rows of pairs without an expert, which order lists behind offsets[-1], are zero in an output
+    that the call makes, and left as they were in a Y of the caller's."""
+    torch = _torch()
+    w = "fp8_gemm_grouped"
+    m, n, count = experts.m, experts.n, experts.experts
+    rows, ldx, ldxs = _fp8_rows(torch, w, n, xq, xs)
+    pairs = rows * int(pairs_per_row)
+    if (pairs | count | m | n) >> 31:
+        raise TgError(-2, w)
+    if order.dtype != torch.int32 or order.shape != (pairs,) or not order.is_contiguous():
+        raise ValueError(f"{w}: expected order int32 [{pairs}]")
+    if offsets.dtype != torch.int32 or offsets.shape != (count + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"{w}: expected offsets int32 [{count + 1}]")
+    at = _common_device(w, xq, xs, experts.q, offsets, order, Y)
+    if stream is not None or at != torch._C._cuda_getDevice():
+        with _Entered(at, stream):
+            return fp8_gemm_grouped(experts, xq, xs, offsets, order, pairs_per_row, Y, out_dtype)
+    zero = TG_ZERO_UNROUTED if Y is None else 0
+    Y, code, ldy = _int8_out(torch, w, Y, pairs, m, out_dtype, xq)
+    status = (_lib or lib()).fp8_gemm_grouped(pairs, count, m, n, xq.data_ptr(), ldx, xs.data_ptr(), ldxs, int(pairs_per_row), experts.q.data_ptr(),
+                                              experts.scales.data_ptr(), offsets.data_ptr(), order.data_ptr(), Y.data_ptr(), code | zero, ldy,
+                                              torch._C._cuda_getCurrentRawStream(at))
+    if status:
+        raise TgError(status, w)
+    return Y
+
+
+class Fp8Linear:
+    """An e4m3 linear layer used like a dense one, beside Int8Linear and TrellisLinear: y = W x over the last axis.
+
+    `forward(x)` takes fp32, fp16 or bf16 activations [..., n] on the device, quantises each 128 neighbours of a row with a scale
+    of their own (fp8_quantize) and returns fp32 [..., m] (fp8_gemm), or out_dtype. The workspace is kept as Int8Linear keeps
+    its own: replaced by a larger one when a row count needs it (the earlier ones live on, for graphs that were captured
+    with them; a call under capture that needs a larger one takes the graph's own, cleared at each replay); calls are ordered
+    on one stream.
+    """
+
+    def __init__(self, layer: "Fp8Layer", out_dtype=None):
+        self.layer, self.out_dtype = layer, out_dtype
+        self._ws, self._earlier = None, []
+
+    def forward(self, x, stream=None):
+        n, m = self.layer.n, self.layer.m
+        _expect(x.dim() > 0 and x.shape[-1] == n, "Fp8Linear", f"expected activations [..., {n}], got {tuple(x.shape)}")
+        if stream is not None or _common_device("Fp8Linear", x, self.layer.q) != _torch()._C._cuda_getDevice():
+            with _Entered(x.get_device(), stream):
+                return self.forward(x)
+        xq, xs = fp8_quantize(x)
+        xq, xs = xq.view(-1, n), xs.view(-1, _blocks(n))
+        ws = self._ws
+        if ws is None or ws.numel() < lib().tg_fp8_workspace_size(xq.shape[0], m, n):
+            ws = fp8_workspace(self.layer, xq.shape[0])
+            if not _torch().cuda.is_current_stream_capturing():   # else its zeros are the graph's, there at its replays alone
+                self._earlier.append(self._ws)
+                self._ws = ws
+        return fp8_gemm(self.layer, xq, xs, out_dtype=self.out_dtype, ws=ws).reshape(x.shape[:-1] + (m,))
 
     __call__ = forward
 

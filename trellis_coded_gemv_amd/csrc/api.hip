@@ -902,3 +902,146 @@ TG_API int32_t int8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int3
   if (misaligned(offsets, 4) || misaligned(order, 4)) return TG_ERR_ALIGN;
   return launch_status(launch_int8_gemm(a, (hipStream_t)stream));
 }
+
+namespace {
+
+// Of e4m3 rows and layers: the product's checks, and the rows' scales.
+int32_t check_fp8_operands(const Product8Args& a) {
+  const int32_t st = check_int8_operands(a);
+  if (st != TG_OK) return st;
+  return a.ldxs >= (a.n + 127) / 128 ? TG_OK : TG_ERR_ARG;
+}
+
+size_t fp8_ws_bytes(int32_t M, int32_t m, int32_t n) {
+  return round_up(kInt8Partials + fp8_partial_bytes(M, m, n), kAlign);
+}
+
+}  // namespace
+
+TG_API int32_t rms_norm(int32_t rows, int32_t n, const void* x, int32_t dtype, int64_t ldx, const void* residual,
+                        int32_t residual_dtype, int64_t ldr, void* total, int64_t ldt, const void* weight,
+                        int32_t weight_dtype, float eps, void* y, int32_t out_dtype, int64_t ldy, float* scales,
+                        int64_t lds, void* stream) {
+  if (rows < 1 || rows > (1 << 24) || n < 1 || n > kNormMaxN) return TG_ERR_SHAPE;
+  if (bad_type(dtype) || bad_type(weight_dtype) || out_dtype < TG_F32 || out_dtype > TG_E4M3 || ldx < n || ldy < n ||
+      !(eps >= 0.f && eps - eps == 0.f))
+    return TG_ERR_ARG;
+  if (residual && (bad_type(residual_dtype) || ldr < n || ldt < n)) return TG_ERR_ARG;
+  const bool scaled = out_dtype == TG_INT8 || out_dtype == TG_E4M3;
+  if (scaled && lds < (out_dtype == TG_INT8 ? 1 : (n + 127) / 128)) return TG_ERR_ARG;
+  if (!x || !weight || !y || (residual && !total) || (scaled && !scales)) return TG_ERR_NULL;
+  if (misaligned(x, type_size(dtype)) || misaligned(weight, type_size(weight_dtype)) ||
+      (!scaled && misaligned(y, type_size(out_dtype))) || (scaled && misaligned(scales, 4)))
+    return TG_ERR_ALIGN;
+  if (residual && (misaligned(residual, type_size(residual_dtype)) || misaligned(total, type_size(residual_dtype))))
+    return TG_ERR_ALIGN;
+  NormArgs a{};
+  a.x = x;
+  a.residual = residual;
+  a.total = total;
+  a.w = weight;
+  a.y = y;
+  a.scales = scales;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldt = ldt;
+  a.ldy = ldy;
+  a.lds = lds;
+  a.rows = rows;
+  a.n = n;
+  a.x_type = dtype;
+  a.r_type = residual_dtype;
+  a.w_type = weight_dtype;
+  a.out = out_dtype;
+  a.eps = eps;
+  return launch_status(launch_rms_norm(a, (hipStream_t)stream));
+}
+
+TG_API int32_t fp8_quantize(int32_t rows, int32_t n, const void* x, int32_t dtype, int64_t ldx, int32_t block_rows,
+                            uint8_t* q, int64_t ldq, float* scales, int64_t lds, void* stream) {
+  if (rows < 1 || rows > (1 << 24) || n < 1 || n > (1 << 22) || (int64_t)rows * n > kMaxDenseWeights) return TG_ERR_SHAPE;
+  if (bad_type(dtype) || (block_rows != 1 && block_rows != 128) || ldx < n || ldq < n || lds < (n + 127) / 128) return TG_ERR_ARG;
+  if (!x || !q || !scales) return TG_ERR_NULL;
+  if (misaligned(x, type_size(dtype)) || misaligned(scales, 4)) return TG_ERR_ALIGN;
+  return launch_status(launch_fp8_quantize(rows, n, x, dtype, ldx, block_rows == 128, q, ldq, scales, lds, (hipStream_t)stream));
+}
+
+TG_API size_t tg_fp8_workspace_size(int32_t M, int32_t m, int32_t n) {
+  return check_int8_shape(M, m, n) == TG_OK ? fp8_ws_bytes(M, m, n) : 0;
+}
+
+TG_API int32_t tg_fp8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_t* plan) {
+  const int32_t st = check_int8_shape(rows, m, n);
+  if (st != TG_OK) return st;
+  if (experts < 0 || experts > kRouteMaxExperts) return TG_ERR_SHAPE;
+  if (!plan) return TG_ERR_NULL;
+  const Int8Plan p = fp8_plan(rows, m, n, experts);
+  plan[0] = p.shape;
+  plan[1] = p.splits;
+  fp8_plan_tile(p, plan + 2, plan + 3);
+  return TG_OK;
+}
+
+TG_API int32_t fp8_gemm(int32_t M, int32_t m, int32_t n, const uint8_t* xq, int64_t ldx, const float* xs, int64_t ldxs,
+                        const uint8_t* wq, int64_t ldw, const float* wscales, void* Y, int32_t out_dtype, int64_t ldy,
+                        void* ws, size_t ws_bytes, void* stream) {
+  int32_t st = check_int8_shape(M, m, n);
+  if (st != TG_OK) return st;
+  Product8Args a{};
+  a.x = reinterpret_cast<const int8_t*>(xq);
+  a.xs = xs;
+  a.w = reinterpret_cast<const int8_t*>(wq);
+  a.ws = wscales;
+  a.y = Y;
+  a.ldx = ldx;
+  a.ldxs = ldxs;
+  a.ldw = ldw;
+  a.ldy = ldy;
+  a.M = M;
+  a.m = m;
+  a.n = n;
+  a.experts = 1;
+  a.pairs_per_row = 1;
+  a.out = out_dtype;
+  st = check_fp8_operands(a);
+  if (st != TG_OK) return st;
+  if (!ws || ws_bytes < fp8_ws_bytes(M, m, n)) return TG_ERR_WORKSPACE;
+  if (misaligned(ws, kAlign)) return TG_ERR_ALIGN;
+  a.counters = reinterpret_cast<uint32_t*>((char*)ws + kWsHeader);
+  a.partials = reinterpret_cast<uint64_t*>((char*)ws + kInt8Partials);
+  return launch_status(launch_fp8_gemm(a, (hipStream_t)stream));
+}
+
+TG_API int32_t fp8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int32_t n, const uint8_t* xq, int64_t ldx,
+                                const float* xs, int64_t ldxs, int32_t pairs_per_row, const uint8_t* wq,
+                                const float* wscales, const int32_t* offsets, const int32_t* order, void* Y,
+                                int32_t out_dtype, int64_t ldy, void* stream) {
+  int32_t st = check_int8_shape(pairs, m, n);
+  if (st != TG_OK) return st;
+  if (experts < 1 || experts > kRouteMaxExperts) return TG_ERR_SHAPE;
+  if (pairs_per_row < 1 || pairs % pairs_per_row != 0) return TG_ERR_ARG;
+  Product8Args a{};
+  a.x = reinterpret_cast<const int8_t*>(xq);
+  a.xs = xs;
+  a.w = reinterpret_cast<const int8_t*>(wq);
+  a.ws = wscales;
+  a.offsets = offsets;
+  a.order = order;
+  a.y = Y;
+  a.ldx = ldx;
+  a.ldxs = ldxs;
+  a.ldw = n;
+  a.ldy = ldy;
+  a.M = pairs;
+  a.m = m;
+  a.n = n;
+  a.experts = experts;
+  a.pairs_per_row = pairs_per_row;
+  a.out = out_dtype & ~TG_ZERO_UNROUTED;
+  a.zero_rest = (out_dtype & TG_ZERO_UNROUTED) != 0;
+  st = check_fp8_operands(a);
+  if (st != TG_OK) return st;
+  if (!offsets || !order) return TG_ERR_NULL;
+  if (misaligned(offsets, 4) || misaligned(order, 4)) return TG_ERR_ALIGN;
+  return launch_status(launch_fp8_gemm(a, (hipStream_t)stream));
+}

@@ -1,0 +1,528 @@
+// Products of e4m3 rows with a scale for each block of 128: Y[r, o] = sum_b xs[r, b] ws[o / 128, b] sum_{i in b} xq[r, i] wq[o, i],
+// for a dense layer and for the experts of routed pairs, by tiles of TO outputs x TX rows.
+//
+// A block's sum leaves the matrix cores and is added to the output's by one fused multiply-add in binary32 with the product
+// of its two scales, in rising order of the blocks; parts of a split inner axis are added in rising order too. So the
+// same call gives the same bits. Which instruction forms a block's sum goes by the output's type:
+//   16 bits  v_mfma_f32_16x16x128_f8f6f4, which aligns eight products at a time to the largest of them and drops what lies
+//            below 2^-13 of it (measured: 2^-16 of the result on normal values, 2^-10 of the sum of the magnitudes at most),
+//            where the type keeps 2^-11 or 2^-8;
+//   32 bits  v_mfma_f32_16x16x32_f16 on the values widened to binary16, which hold them exactly: sums of binary32 (2^-26 of
+//            the result on normal values), at half of the rate of the matrix cores. Products of few rows wait for the layer's bytes in
+//            either form.
+//
+// The layer's rows are the A operand and the activation rows the B operand: lane l supplies row l % 16 and, of 128 bytes of
+// the inner axis, the 16 at 16 (l / 16) and the 16 at 64 + 16 (l / 16) on both sides, and ends with four neighbouring outputs of row
+// l % 16. Both sides and the scales reach LDS by loads that do not pass through registers, a ring of ST steps of BK bytes.
+#include <type_traits>
+
+#include "product_tiles.hpp"
+
+namespace tg {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+namespace {
+
+__device__ __forceinline__ void put_partial(uint64_t* p, f32x4 v) {
+  const u32x4 u = __builtin_bit_cast(u32x4, v);
+  __hip_atomic_store(p, (uint64_t)u[1] << 32 | u[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(p + 1, (uint64_t)u[3] << 32 | u[2], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ f32x4 get_partial(uint64_t* p) {
+  const uint64_t a = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint64_t b = __hip_atomic_load(p + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return __builtin_bit_cast(f32x4, u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32)});
+}
+
+// 4 bytes of global memory per lane to LDS at base + 4 * lane, as load_to_lds.
+__device__ __forceinline__ void load4_to_lds(const float* p, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(lds_base), "v"(p) : "m0", "memory");
+}
+
+// Eight e4m3 values as binary16, which holds every one of them.
+__device__ __forceinline__ f16x8 widen(int lo, int hi) {
+  const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
+  const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+  return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// A step's scales in LDS: every wave brings a slot of 64 floats. Its first PER hold its part of the rows' scales, numbered
+// ((u WX + wx) 16 + j) RX + r for block u of the step and row 16 (WX r + wx) + j of the tile, so that a lane finds its rows' as
+// neighbours; behind them the layer's scales of the wave's own outputs, one for each block of the step.
+template <class S>
+struct ScaleSlots {
+  static constexpr int U = S::BK / 128;
+  static constexpr int PER = S::TX * U / S::NW;
+  static constexpr int BUF = S::NW * 256;        // LDS bytes of a step
+  static_assert(S::BK % 128 == 0 && PER * S::NW == S::TX * U && PER % S::RX == 0 && PER + U <= 64, "");
+  static __device__ __forceinline__ int slot(int value) { return value / PER * 64 + value % PER; }
+};
+
+}  // namespace
+
+template <class S, int DT>
+__global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Product8Args a, int out_tiles, int row_tiles) {
+  constexpr int AT = S::AT, RX = S::RX, BK = S::BK, ST = S::ST, TO = S::TO, TX = S::TX, NW = S::NW;
+  using Slots = ScaleSlots<S>;
+  constexpr int U = Slots::U, EW = S::EW, SLDS = S::XLDS + ST * S::XBUF;
+  constexpr bool WIDE = DT == kF32;
+  constexpr bool STREAM = AT * RX >= 16;         // registers for one set of operands beside the sums
+  __shared__ __attribute__((aligned(1024))) int8_t sh[SLDS + ST * Slots::BUF];
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const int j = lane & 15, g = lane >> 4;
+  const Tile tile = find_tile(a, out_tiles, row_tiles, TX);
+  if (tile.count <= 0) return;
+  const int ot = tile.ot, rt = tile.rt, sp = tile.sp;
+  const int o0 = ot * TO;
+  if (tile.expert < 0) {                         // eight neighbouring outputs to a thread
+    const float zeros[8] = {};
+    for (int i = threadIdx.x; i < tile.count * (TO / 8); i += 64 * NW) {
+      const int pair = pair_of(a, tile, i / (TO / 8)), o = o0 + i % (TO / 8) * 8;
+      if (pair >= 0 && o < a.m) store_outputs<DT, 8>(a.y, (int64_t)pair * a.ldy + o, zeros, a.m - o);
+    }
+    return;
+  }
+  const int wo = wave % S::WO, wx = wave / S::WO;
+
+  // Loads: an instruction fills RPI rows of LDS; lane l the slot l % (BK / 16) of row l / (BK / 16), where the piece
+  // slot ^ swizzle(row) of the row belongs.
+  const int lrow = lane / (BK / 16);
+  auto wrow = [&](int i) { return S::RPI * (S::LW * wave + i) + lrow; };   // LDS row of this lane in instruction i
+  auto xrow = [&](int i) { return S::RPI * (S::LX * wave + i) + lrow; };
+  auto piece = [&](int row) { return 16 * ((lane % (BK / 16)) ^ S::swizzle(row)); };
+  auto source = [&](int i) { return (int64_t)(max(pair_of(a, tile, i), 0) / a.pairs_per_row); };   // activation row of the tile's row i
+  // The layer's rows are addressed by 32-bit offsets to the tile's first row (the launch keeps their stride below 2^23).
+  const int8_t* wbase = a.w + ((int64_t)tile.expert * a.m + o0) * a.ldw;
+  uint32_t woff[S::LW];
+  const int8_t* xp[S::LX];
+#pragma unroll
+  for (int i = 0; i < S::LW; ++i) woff[i] = (uint32_t)min(lds_row_output(AT, wrow(i)), a.m - 1 - o0) * (uint32_t)a.ldw;
+#pragma unroll
+  for (int i = 0; i < S::LX; ++i) xp[i] = a.x + source(xrow(i)) * a.ldx;
+  const int blocks = (a.n + 127) >> 7;           // of the inner axis
+  const float* sp0;                              // where the lane's scale of block 0 of a step lies for step 0
+  int su;                                        // which block of a step it is
+  {
+    const int v = wave * Slots::PER + min(lane, Slots::PER - 1), r = v % RX, vj = v / RX % 16, uw = v / (16 * RX);
+    const int ob = min((o0 + 16 * AT * wo) >> 7, (a.m - 1) >> 7);
+    const bool own = lane >= Slots::PER;
+    su = own ? min(lane - Slots::PER, U - 1) : uw / S::WX;
+    sp0 = own ? a.ws + ((int64_t)tile.expert * ((a.m + 127) >> 7) + ob) * blocks
+              : a.xs + source(16 * (S::WX * r + uw % S::WX) + vj) * a.ldxs;
+  }
+  const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)sh;
+  const uint32_t wfill = __builtin_amdgcn_readfirstlane(sh0 + wave * S::LW * 1024);
+  const uint32_t xfill = __builtin_amdgcn_readfirstlane(sh0 + S::XLDS + wave * S::LX * 1024);
+  const uint32_t sfill = __builtin_amdgcn_readfirstlane(sh0 + SLDS + wave * 256);
+  auto load_w = [&](int step, uint32_t buf) {
+    const int k = step * BK, most = a.n - 16 - k;    // pieces past the end: any bytes of the row, not multiplied
+#pragma unroll
+    for (int i = 0; i < S::LW; ++i) load_to_lds(wbase, woff[i] + (uint32_t)(k + min(piece(wrow(i)), most)), wfill + buf * S::WBUF + i * 1024);
+  };
+  auto load_x = [&](int step, uint32_t buf) {        // and the scales
+    const int k = step * BK, most = a.n - 16 - k;
+#pragma unroll
+    for (int i = 0; i < S::LX; ++i) load_to_lds(xp[i] + (k + min(piece(xrow(i)), most)), xfill + buf * S::XBUF + i * 1024);
+    load4_to_lds(sp0 + min(step * U + su, blocks - 1), sfill + buf * Slots::BUF);
+  };
+
+  f32x4 acc[AT][RX];
+#pragma unroll
+  for (int t = 0; t < AT; ++t)
+#pragma unroll
+    for (int r = 0; r < RX; ++r) acc[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int slot = 16 * (g ^ S::swizzle(j));     // of the step's first 64 bytes; the h-th 64: slot ^ 64 h
+  const int abase = (wo * 16 * AT + j) * BK + slot, bbase = S::XLDS + (wx * 16 + j) * BK + slot;
+  const int steps_all = (a.n + BK - 1) / BK;
+  const int begin = (int)((int64_t)steps_all * sp / a.splits), end = (int)((int64_t)steps_all * (sp + 1) / a.splits);
+  int s = begin;
+  uint32_t wbuf = 0, xbuf = 0;                   // of step s
+  auto advance = [&]() {
+    wbuf = wbuf == (uint32_t)(ST + EW - 1) ? 0u : wbuf + 1u;
+    xbuf = xbuf == (uint32_t)(ST - 1) ? 0u : xbuf + 1u;
+  };
+  // Reads of block u of step s.
+  auto both = [&](int at, int u) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(sh + (at ^ (128 * u))), hi = *reinterpret_cast<const i32x4*>(sh + (at ^ (128 * u + 64)));
+    return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  auto read_w = [&](int t, int u) { return both(wbuf * S::WBUF + abase + t * 16 * BK, u); };
+  auto read_x = [&](int r, int u) { return both(xbuf * S::XBUF + bbase + r * S::WX * 16 * BK, u); };
+  auto scales = [&]() { return reinterpret_cast<const float*>(sh + SLDS + xbuf * Slots::BUF); };
+  auto read_xs = [&](int r, int u) { return scales()[Slots::slot(((u * S::WX + wx) * 16 + j) * RX) + r]; };
+  auto read_ws = [&](int u) { return scales()[wave * 64 + Slots::PER + u]; };
+  auto cut = [&](i32x8& b, int left) {           // pieces past the end of the inner axis count as zero
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (64 * h + 16 * g >= left) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) b[4 * h + d] = 0;
+      }
+  };
+  // The sums of a block for one tile of 16 rows.
+  struct Wide {
+    f16x8 q[4];
+  };
+  auto widen_all = [&](const i32x8& v) {
+    Wide w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w.q[q] = widen(v[2 * q], v[2 * q + 1]);
+    return w;
+  };
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  auto product = [&](const i32x8& w, const i32x8& x) { return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 0, 0, 0); };
+  auto wide_products = [&](f32x4 (&p)[AT], const Wide (&w)[AT], const Wide& x) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int t = 0; t < AT; ++t) p[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t].q[q], x.q[q], q == 0 ? zero : p[t], 0, 0, 0);
+  };
+  auto add = [&](f32x4& sum, const f32x4& p, float scale) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sum[c] = fmaf(p[c], scale, sum[c]);
+  };
+
+  // Loads in the order X(i) with its scales, W(i + EW): kAhead may still be in flight when X(i) and W(i) are needed.
+  constexpr int kStep = S::LW + S::LX + 1, kAhead = (EW > 0 ? S::LW : 0) + (ST - 1) * kStep;
+  auto first_loads = [&]() {
+    if constexpr (EW > 0) load_w(begin, 0);
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+      load_x(min(begin + i, end - 1), i);
+      load_w(min(begin + i + EW, end - 1), i + EW);
+    }
+    wait_loads<kAhead>();
+    __builtin_amdgcn_s_barrier();
+  };
+  // On to the next step: its loads have landed and every wave holds the rest of this one in registers, so this step's buffers
+  // are free for loads.
+  auto next_step = [&](auto more) {
+    wait_loads<decltype(more)::value ? kAhead - kStep : 0>();
+    __builtin_amdgcn_s_barrier();
+    if constexpr (decltype(more)::value) {
+      load_x(s + ST, xbuf);
+      load_w(min(s + ST + EW, end - 1), wbuf);
+    }
+    advance();
+    ++s;
+  };
+  using More = std::true_type;
+  using Rest = std::false_type;
+
+  // Large tiles: the layer's operands of a block stay in registers, those of the rows come one tile of 16 ahead, and the sums of a
+  // tile of 16 rows are added up while the matrix cores work on the next.
+  auto stream_loop = [&](auto rows) __attribute__((always_inline)) {
+    constexpr int R = decltype(rows)::value;
+    static_assert(U == 1 && R % 2 == 0, "");
+    i32x8 w[AT], x[2];
+    f32x4 p[2][AT];
+    float xs[2], ws, before = 0.f;               // before: the scale of the sums in hand
+#pragma unroll
+    for (int t = 0; t < AT; ++t) p[1][t] = zero;
+    first_loads();
+    auto read_first = [&](auto last) {
+      if constexpr (!decltype(last)::value) {
+        xs[0] = read_xs(0, 0);
+        ws = read_ws(0);
+        x[0] = read_x(0, 0);
+      }
+    };
+    read_first(std::false_type{});
+#pragma unroll
+    for (int t = 0; t < AT; ++t) w[t] = read_w(t, 0);
+    auto step = [&](auto last, auto more) __attribute__((always_inline)) {
+      constexpr bool LAST = decltype(last)::value;
+      const int left = LAST ? a.n - s * BK : BK;
+      if constexpr (LAST) cut(x[0], left);
+      Wide ww[WIDE ? AT : 1];
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int t = 0; t < AT; ++t) ww[t] = widen_all(w[t]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int cur = r & 1;
+        const float scale = xs[cur] * ws;
+        if (r < R - 1) {
+          xs[cur ^ 1] = read_xs(r + 1, 0);
+          x[cur ^ 1] = read_x(r + 1, 0);
+          if constexpr (LAST) cut(x[cur ^ 1], left);
+        } else if constexpr (!LAST) {
+          next_step(more);
+          read_first(last);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (WIDE) {
+          wide_products(p[cur], ww, widen_all(x[cur]));
+#pragma unroll
+          for (int t = 0; t < AT; ++t) {
+            add(acc[t][(r + R - 1) % R], p[cur ^ 1][t], before);
+            if (!LAST && r == R - 1) w[t] = read_w(t, 0);
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < AT; ++t) {
+            p[cur][t] = product(w[t], x[cur]);
+            if (!LAST && r == R - 1) w[t] = read_w(t, 0);
+            add(acc[t][(r + R - 1) % R], p[cur ^ 1][t], before);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        before = scale;
+      }
+    };
+    while (s < end - ST) step(std::false_type{}, More{});
+    while (s < end - 1) step(std::false_type{}, Rest{});
+    step(std::true_type{}, Rest{});
+#pragma unroll
+    for (int t = 0; t < AT; ++t) add(acc[t][R - 1], p[1][t], before);
+  };
+
+  // Small tiles: the operands and scales of a block are read while the matrix cores work on the block before.
+  struct Frags {
+    i32x8 w[AT], x[RX];
+    float xs[RX], ws;
+  };
+  auto ahead_loop = [&](auto rows) __attribute__((always_inline)) {
+    constexpr int R = decltype(rows)::value;
+    Frags f[2];
+    auto read = [&](Frags& f, int u) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        f.x[r] = read_x(r, u);
+        f.xs[r] = read_xs(r, u);
+      }
+      f.ws = read_ws(u);
+#pragma unroll
+      for (int t = 0; t < AT; ++t) f.w[t] = read_w(t, u);
+    };
+    auto multiply = [&](const Frags& f) {
+      Wide ww[WIDE ? AT : 1];
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int t = 0; t < AT; ++t) ww[t] = widen_all(f.w[t]);
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        f32x4 p[AT];
+        if constexpr (WIDE) {
+          wide_products(p, ww, widen_all(f.x[r]));
+        } else {
+#pragma unroll
+          for (int t = 0; t < AT; ++t) p[t] = product(f.w[t], f.x[r]);
+        }
+#pragma unroll
+        for (int t = 0; t < AT; ++t) add(acc[t][r], p[t], f.xs[r] * f.ws);
+      }
+    };
+    first_loads();
+    read(f[0], 0);
+    auto step = [&](auto more, auto first) __attribute__((always_inline)) {     // from set `first` on
+      constexpr int F = decltype(first)::value;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u == U - 1) next_step(more);
+        read(f[(F + u + 1) & 1], (u + 1) % U);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(f[(F + u) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    using Even = std::integral_constant<int, 0>;
+    using Odd = std::integral_constant<int, 1>;
+    if constexpr (U % 2 == 0) {
+      while (s < end - ST) step(More{}, Even{});
+    } else {
+      while (s < end - ST - 1) {
+        step(More{}, Even{});
+        step(More{}, Odd{});
+      }
+      if (s < end - ST) {
+        step(More{}, Even{});
+        f[0] = f[1];
+      }
+    }
+    while (s < end - 1) {
+      step(Rest{}, Even{});
+      if constexpr (U % 2 == 1) f[0] = f[1];
+    }
+    const int left = a.n - s * BK;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (128 * u >= left) break;
+      if (u < U - 1) read(f[(u + 1) & 1], u + 1);
+#pragma unroll
+      for (int r = 0; r < R; ++r) cut(f[u & 1].x[r], left - 128 * u);
+      multiply(f[u & 1]);
+    }
+  };
+  auto main_loop = [&](auto rows) __attribute__((always_inline)) {
+    if constexpr (STREAM) stream_loop(rows);
+    else ahead_loop(rows);
+  };
+  // The rows' tiles of 16 go round the waves, and a wave multiplies all of its own, half or a quarter, as the tile has rows.
+  const int there = ((tile.count + 15) / 16 - wx + S::WX - 1) / S::WX;
+  constexpr int kLeast = STREAM ? 2 : 1;         // the streaming loop takes them in pairs
+  if constexpr (RX / 2 >= kLeast) {
+    if (there > RX / 2) {
+      main_loop(std::integral_constant<int, RX>{});
+    } else {
+      if constexpr (RX / 4 >= kLeast) {
+        if (there > RX / 4) main_loop(std::integral_constant<int, RX / 2>{});
+        else main_loop(std::integral_constant<int, RX / 4>{});
+      } else {
+        main_loop(std::integral_constant<int, RX / 2>{});
+      }
+    }
+  } else {
+    main_loop(std::integral_constant<int, RX>{});
+  }
+  wait_loads<0>();
+
+  // Split inner axis: every workgroup of the tile leaves its sums, the last to arrive adds all of them, the first part's first,
+  // and goes on.
+  if (a.splits > 1) {
+    constexpr int T = 64 * NW;
+    uint64_t* first = a.partials + (size_t)(rt * out_tiles + ot) * a.splits * (2 * T * AT * RX) + 2 * threadIdx.x;
+#pragma unroll
+    for (int t = 0; t < AT; ++t)
+#pragma unroll
+      for (int r = 0; r < RX; ++r) put_partial(first + (size_t)sp * (2 * T * AT * RX) + 2 * T * (t * RX + r), acc[t][r]);
+    __syncthreads();                              // the operands' LDS is done with: its first word is the flag
+    if (!arrive_is_last(a.counters + rt * out_tiles + ot, a.splits, reinterpret_cast<uint32_t*>(sh))) return;
+    for (int o = 0; o < a.splits; ++o) {
+      uint64_t* part = first + (size_t)o * (2 * T * AT * RX);
+#pragma unroll
+      for (int t = 0; t < AT; ++t)
+#pragma unroll
+        for (int r = 0; r < RX; ++r) {
+          const f32x4 v = get_partial(part + 2 * T * (t * RX + r));
+          acc[t][r] = o == 0 ? v : acc[t][r] + v;
+        }
+    }
+    if (threadIdx.x == 0) reset_counter(a.counters + rt * out_tiles + ot);
+  }
+
+  const int ob = o0 + 16 * AT * wo;
+  int pair[RX];
+#pragma unroll
+  for (int r = 0; r < RX; ++r) pair[r] = pair_of(a, tile, 16 * (S::WX * r + wx) + j);
+  constexpr int N = AT == 1 ? 4 : 8;
+#pragma unroll
+  for (int r = 0; r < RX; ++r) {
+    if (pair[r] < 0) continue;
+#pragma unroll
+    for (int t = 0; t < AT; t += N / 4) {
+      const int o = ob + S::output(t, g);
+      if (o >= a.m) continue;
+      float v[N];
+#pragma unroll
+      for (int c = 0; c < N; ++c) v[c] = acc[t + c / 4][r][c % 4];
+      store_outputs<DT, N>(a.y, (int64_t)pair[r] * a.ldy + o, v, a.m - o);
+    }
+  }
+}
+
+template <class S, int DT>
+static hipError_t launch_shape_t(const Product8Args& a, hipStream_t s) {
+  const int ot = (a.m + S::TO - 1) / S::TO, rt = row_tiles(a, S::TX);
+  const int64_t groups = (int64_t)ot * rt * a.splits + (a.zero_rest ? 8 : 0);   // 8: as zeros_number asks
+  if (groups >= (int64_t)1 << 31) return hipErrorInvalidConfiguration;   // no accepted shape has as many
+  const dim3 grid((unsigned)(groups < kGridWidth ? groups : kGridWidth), (unsigned)((groups + kGridWidth - 1) / kGridWidth));
+  hipLaunchKernelGGL((fp8_tile_kernel<S, DT>), grid, dim3(64 * S::NW), 0, s, a, ot, rt);
+  return hipGetLastError();
+}
+
+template <class S>
+static hipError_t launch_shape(const Product8Args& a, hipStream_t s) {
+  if (a.out == kF32) return launch_shape_t<S, kF32>(a, s);
+  if (a.out == kF16) return launch_shape_t<S, kF16>(a, s);
+  return launch_shape_t<S, kBf16>(a, s);
+}
+
+// The tile shapes. What one costs: microseconds per 128 bytes of the inner axis for a compute unit that holds one workgroup, and
+// for one that holds two; microseconds per tile beside that (its first loads, its stores).
+struct TileCost {
+  int out, rows, resident;
+  float alone, shared, tile;
+};
+constexpr TileCost kTiles[] = {
+    {256, 256, 1, 1.484f, 1.484f, 5.05f}, // TileShape<4, 8, 4, 2, 128, 2>
+    {256, 128, 1, 0.974f, 0.974f, 4.26f}, // TileShape<4, 4, 4, 2, 128, 3>
+    {128, 128, 1, 0.533f, 0.533f, 2.24f}, // TileShape<2, 4, 4, 2, 128, 3>
+    {128, 64, 2, 0.321f, 0.677f, 2.28f},  // TileShape<2, 4, 4, 1, 128, 3>
+    {64, 32, 2, 0.124f, 0.222f, 1.13f},   // TileShape<1, 2, 4, 1, 256, 3>
+    {32, 16, 2, 0.047f, 0.14f, 0.85f},    // TileShape<1, 1, 2, 1, 512, 3>
+};
+constexpr float kStreamRate = 5.3e6f;   // bytes per microsecond of a product that waits for memory alone
+
+// The cheapest shape and split of the inner axis: rounds of workgroups over the compute units, and the time that the
+// bytes take, of which a part is not hidden behind the other. Experts: row tiles as an even routing fills them, one half-filled
+// for each expert.
+Int8Plan fp8_plan(int M, int m, int n, int experts) {
+  const float reached = experts > 0 ? (float)(experts < M ? experts : M) : 1.f;
+  const float rows = (float)M / reached;
+  const float stream = (reached * m * (float)n + (float)M * n + 2.f * M * m) / kStreamRate;
+  const int steps = (n + 127) / 128;
+  Int8Plan best{0, 1};
+  float least = 3.0e38f;
+  for (int shape = 0; shape < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++shape) {
+    const TileCost& t = kTiles[shape];
+    if (t.rows > 32 && t.rows > 2.f * rows) continue;          // more than half of it empty
+    const float rt = experts > 0 ? reached * (rows / t.rows + 0.5f > 1.f ? rows / t.rows + 0.5f : 1.f)
+                                 : (float)((M + t.rows - 1) / t.rows);
+    const float tiles = rt * (float)((m + t.out - 1) / t.out);
+    const int slots = kComputeUnits * t.resident;
+    for (int splits : {1, 2, 3, 4, 6, 8}) {
+      if (splits > 1 && (experts > 0 || tiles > kInt8Counters / 2 || splits * 512 > n)) break;
+      const float groups = tiles * splits;
+      const float rounds = (float)(int64_t)(groups / slots), rest = groups - rounds * slots;
+      const float len = (float)((steps + splits - 1) / splits);
+      float work = rounds * (t.shared * len + t.tile);
+      if (rest > 0.f) work += (rest > kComputeUnits ? t.shared : t.alone) * len + t.tile;
+      float us = (work > stream ? work : stream) + 0.2f * (work > stream ? stream : work);
+      if (splits > 1) us += 0.9f + 2.1e-6f * splits * M * m;
+      if (us < least) {
+        least = us;
+        best = {shape, splits};
+      }
+    }
+  }
+  return best;
+}
+
+void fp8_plan_tile(const Int8Plan& p, int* outputs, int* rows) {
+  *outputs = kTiles[p.shape].out;
+  *rows = kTiles[p.shape].rows;
+}
+
+size_t fp8_partial_bytes(int M, int m, int n) {
+  const Int8Plan p = fp8_plan(M, m, n, 0);
+  if (p.splits <= 1) return 0;
+  const TileCost& t = kTiles[p.shape];
+  return (size_t)((m + t.out - 1) / t.out) * ((M + t.rows - 1) / t.rows) * p.splits * t.out * t.rows * 4;
+}
+
+hipError_t launch_fp8_gemm(const Product8Args& args, hipStream_t s) {
+  Product8Args a = args;
+  const Int8Plan p = fp8_plan(a.M, a.m, a.n, a.offsets ? a.experts : 0);
+  a.splits = p.splits;
+  switch (p.shape) {
+    case 0: return launch_shape<TileShape<4, 8, 4, 2, 128, 2>>(a, s);
+    case 1: return launch_shape<TileShape<4, 4, 4, 2, 128, 3>>(a, s);
+    case 2: return launch_shape<TileShape<2, 4, 4, 2, 128, 3>>(a, s);
+    case 3: return launch_shape<TileShape<2, 4, 4, 1, 128, 3>>(a, s);
+    case 4: return launch_shape<TileShape<1, 2, 4, 1, 256, 3>>(a, s);
+    case 5: return launch_shape<TileShape<1, 1, 2, 1, 512, 3>>(a, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace tg

@@ -153,11 +153,12 @@ struct Product8Args {
   const int8_t* x;
   const float* xs;
   const int8_t* w;        // [experts][m] rows
-  const float* ws;        // [experts][m]
+  const float* ws;        // [experts][m]; e4m3: [experts][m / 128][n / 128], rounded up
   const int32_t* offsets; // [experts + 1], or null: dense
   const int32_t* order;   // [M] pairs in expert order
   void* y;
   int64_t ldx, ldw, ldy;
+  int64_t ldxs;           // e4m3: floats from a row's scales to the next's
   int32_t M, m, n;        // M: output rows (pairs)
   int32_t experts, pairs_per_row;
   int32_t out;            // kF32, kF16, kBf16
@@ -168,7 +169,7 @@ struct Product8Args {
 };
 // The kernel and the split of the inner axis that a product takes.
 struct Int8Plan {
-  int shape;              // a tile shape of int8_gemm.hip
+  int shape;              // a tile shape of int8_gemm.hip or fp8_gemm.hip
   int splits;
 };
 Int8Plan int8_plan(int M, int m, int n, int experts);   // experts 0: a dense product
@@ -179,6 +180,29 @@ size_t int8_partial_bytes(int M, int m, int n);
 hipError_t launch_int8_quantize(int rows, int n, const void* x, int dtype, int64_t ldx, int8_t* q, int64_t ldq,
                                 float* scales, hipStream_t s);
 hipError_t launch_int8_gemm(const Product8Args& a, hipStream_t s);
+Int8Plan fp8_plan(int M, int m, int n, int experts);
+void fp8_plan_tile(const Int8Plan& p, int* outputs, int* rows);
+size_t fp8_partial_bytes(int M, int m, int n);
+hipError_t launch_fp8_quantize(int rows, int n, const void* x, int dtype, int64_t ldx, bool layer, uint8_t* q, int64_t ldq,
+                               float* scales, int64_t lds, hipStream_t s);
+hipError_t launch_fp8_gemm(const Product8Args& a, hipStream_t s);
+
+// Root-mean-square norm (rms_norm.hip). Its outputs are of the types above, int8 or e4m3 (TG_INT8, TG_E4M3).
+constexpr int kInt8 = 3, kE4m3 = 4;
+constexpr int kNormMaxN = 32768;         // a row stays in the registers of 1024 threads
+struct NormArgs {
+  const void* x;
+  const void* residual;   // or null
+  void* total;            // x + residual, in the residual's type
+  const void* w;
+  void* y;
+  float* scales;          // int8: one for each row; e4m3: one for each 128 values
+  int64_t ldx, ldr, ldt, ldy, lds;
+  int32_t rows, n;
+  int32_t x_type, r_type, w_type, out;
+  float eps;
+};
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s);
 constexpr int kEncMaxSlots = 256;        // encoder workgroups in flight (one tile each at a time)
 
 // LDS bytes a GEMV workgroup needs for a chunk of `chunk_blocks` 128-blocks.

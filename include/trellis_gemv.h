@@ -649,8 +649,8 @@ int32_t fp8_gemm_grouped(int32_t pairs, int32_t experts, int32_t m, int32_t n, c
                          const int32_t *offsets, const int32_t *order, void *Y, int32_t out_dtype, int64_t ldy,
                          void *stream);
 
-/* The kernel that an e4m3 product of this shape takes, as tg_int8_plan. */
-int32_t tg_fp8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_t *plan);
+/* The kernel that an e4m3 product of this shape and output type takes, as tg_int8_plan. */
+int32_t tg_fp8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_t out_dtype, int32_t *plan);
 
 #ifdef __cplusplus
 }

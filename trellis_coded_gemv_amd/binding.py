@@ -112,7 +112,7 @@ def lib() -> ctypes.CDLL:
         "fp8_gemm": (I32, [I32, I32, I32, P, I64, P, I64, P, I64, P, P, I32, I64, P, SZ, P]),
         "tg_fp8_workspace_size": (SZ, [I32, I32, I32]),
         "fp8_gemm_grouped": (I32, [I32, I32, I32, I32, P, I64, P, I64, I32, P, P, P, P, P, I32, I64, P]),
-        "tg_fp8_plan": (I32, [I32, I32, I32, I32, ctypes.POINTER(I32)]),
+        "tg_fp8_plan": (I32, [I32, I32, I32, I32, I32, ctypes.POINTER(I32)]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)

@@ -970,12 +970,13 @@ TG_API size_t tg_fp8_workspace_size(int32_t M, int32_t m, int32_t n) {
   return check_int8_shape(M, m, n) == TG_OK ? fp8_ws_bytes(M, m, n) : 0;
 }
 
-TG_API int32_t tg_fp8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_t* plan) {
+TG_API int32_t tg_fp8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_t out_dtype, int32_t* plan) {
   const int32_t st = check_int8_shape(rows, m, n);
   if (st != TG_OK) return st;
   if (experts < 0 || experts > kRouteMaxExperts) return TG_ERR_SHAPE;
+  if (bad_type(out_dtype)) return TG_ERR_ARG;
   if (!plan) return TG_ERR_NULL;
-  const Int8Plan p = fp8_plan(rows, m, n, experts);
+  const Int8Plan p = fp8_plan(rows, m, n, experts, out_dtype == TG_F32);
   plan[0] = p.shape;
   plan[1] = p.splits;
   fp8_plan_tile(p, plan + 2, plan + 3);

@@ -70,9 +70,9 @@ template <class S, int DT>
 __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Product8Args a, int out_tiles, int row_tiles) {
   constexpr int AT = S::AT, RX = S::RX, BK = S::BK, ST = S::ST, TO = S::TO, TX = S::TX, NW = S::NW;
   using Slots = ScaleSlots<S>;
-  constexpr int U = Slots::U, EW = S::EW, SLDS = S::XLDS + ST * S::XBUF;
+  constexpr int U = Slots::U, SLDS = S::XLDS + ST * S::XBUF;
   constexpr bool WIDE = DT == kF32;
-  constexpr bool STREAM = AT * RX >= 16;         // registers for one set of operands beside the sums
+  constexpr bool LARGE = AT * RX >= 16;          // registers for one set of operands beside the sums
   __shared__ __attribute__((aligned(1024))) int8_t sh[SLDS + ST * Slots::BUF];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int j = lane & 15, g = lane >> 4;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
   // slot ^ swizzle(row) of the row belongs.
   const int lrow = lane / (BK / 16);
   auto wrow = [&](int i) { return S::RPI * (S::LW * wave + i) + lrow; };   // LDS row of this lane in instruction i
-  auto xrow = [&](int i) { return S::RPI * (S::LX * wave + i) + lrow; };
+  auto xrow = [&](int i) { return S::RPI * (NW * i + wave) + lrow; };
   auto piece = [&](int row) { return 16 * ((lane % (BK / 16)) ^ S::swizzle(row)); };
   auto source = [&](int i) { return (int64_t)(max(pair_of(a, tile, i), 0) / a.pairs_per_row); };   // activation row of the tile's row i
   // The layer's rows are addressed by 32-bit offsets to the tile's first row (the launch keeps their stride below 2^23).
@@ -118,19 +118,20 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
   }
   const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)sh;
   const uint32_t wfill = __builtin_amdgcn_readfirstlane(sh0 + wave * S::LW * 1024);
-  const uint32_t xfill = __builtin_amdgcn_readfirstlane(sh0 + S::XLDS + wave * S::LX * 1024);
+  const uint32_t xfill = __builtin_amdgcn_readfirstlane(sh0 + S::XLDS + wave * 1024);
   const uint32_t sfill = __builtin_amdgcn_readfirstlane(sh0 + SLDS + wave * 256);
-  auto load_w = [&](int step, uint32_t buf) {
+  auto load_w = [&](int step, uint32_t buf, int from, int to) {
     const int k = step * BK, most = a.n - 16 - k;    // pieces past the end: any bytes of the row, not multiplied
 #pragma unroll
-    for (int i = 0; i < S::LW; ++i) load_to_lds(wbase, woff[i] + (uint32_t)(k + min(piece(wrow(i)), most)), wfill + buf * S::WBUF + i * 1024);
+    for (int i = from; i < to; ++i)
+      load_to_lds(wbase, woff[i] + (uint32_t)(k + min(piece(wrow(i)), most)), wfill + buf * S::WBUF + i * 1024);
   };
-  auto load_x = [&](int step, uint32_t buf) {        // and the scales
+  auto load_x = [&](int step, uint32_t buf, int from, int to) {
     const int k = step * BK, most = a.n - 16 - k;
 #pragma unroll
-    for (int i = 0; i < S::LX; ++i) load_to_lds(xp[i] + (k + min(piece(xrow(i)), most)), xfill + buf * S::XBUF + i * 1024);
-    load4_to_lds(sp0 + min(step * U + su, blocks - 1), sfill + buf * Slots::BUF);
+    for (int i = from; i < to; ++i) load_to_lds(xp[i] + (k + min(piece(xrow(i)), most)), xfill + buf * S::XBUF + i * (NW * 1024));
   };
+  auto load_s = [&](int step, uint32_t buf) { load4_to_lds(sp0 + min(step * U + su, blocks - 1), sfill + buf * Slots::BUF); };
 
   f32x4 acc[AT][RX];
 #pragma unroll
@@ -142,19 +143,15 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
   const int steps_all = (a.n + BK - 1) / BK;
   const int begin = (int)((int64_t)steps_all * sp / a.splits), end = (int)((int64_t)steps_all * (sp + 1) / a.splits);
   int s = begin;
-  uint32_t wbuf = 0, xbuf = 0;                   // of step s
-  auto advance = [&]() {
-    wbuf = wbuf == (uint32_t)(ST + EW - 1) ? 0u : wbuf + 1u;
-    xbuf = xbuf == (uint32_t)(ST - 1) ? 0u : xbuf + 1u;
-  };
+  uint32_t buf = 0;                              // of step s
   // Reads of block u of step s.
   auto both = [&](int at, int u) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(sh + (at ^ (128 * u))), hi = *reinterpret_cast<const i32x4*>(sh + (at ^ (128 * u + 64)));
     return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
-  auto read_w = [&](int t, int u) { return both(wbuf * S::WBUF + abase + t * 16 * BK, u); };
-  auto read_x = [&](int r, int u) { return both(xbuf * S::XBUF + bbase + r * S::WX * 16 * BK, u); };
-  auto scales = [&]() { return reinterpret_cast<const float*>(sh + SLDS + xbuf * Slots::BUF); };
+  auto read_w = [&](int t, int u) { return both(buf * S::WBUF + abase + t * 16 * BK, u); };
+  auto read_x = [&](int r, int u) { return both(buf * S::XBUF + bbase + r * S::WX * 16 * BK, u); };
+  auto scales = [&]() { return reinterpret_cast<const float*>(sh + SLDS + buf * Slots::BUF); };
   auto read_xs = [&](int r, int u) { return scales()[Slots::slot(((u * S::WX + wx) * 16 + j) * RX) + r]; };
   auto read_ws = [&](int u) { return scales()[wave * 64 + Slots::PER + u]; };
   auto cut = [&](i32x8& b, int left) {           // pieces past the end of the inner axis count as zero
@@ -165,8 +162,7 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
         for (int d = 0; d < 4; ++d) b[4 * h + d] = 0;
       }
   };
-  // The sums of a block for one tile of 16 rows.
-  struct Wide {
+  struct Wide {                                  // an operand widened
     f16x8 q[4];
   };
   auto widen_all = [&](const i32x8& v) {
@@ -177,49 +173,54 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
   };
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   auto product = [&](const i32x8& w, const i32x8& x) { return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 0, 0, 0); };
-  auto wide_products = [&](f32x4 (&p)[AT], const Wide (&w)[AT], const Wide& x) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int t = 0; t < AT; ++t) p[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t].q[q], x.q[q], q == 0 ? zero : p[t], 0, 0, 0);
-  };
   auto add = [&](f32x4& sum, const f32x4& p, float scale) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) sum[c] = fmaf(p[c], scale, sum[c]);
   };
 
-  // Loads in the order X(i) with its scales, W(i + EW): kAhead may still be in flight when X(i) and W(i) are needed.
-  constexpr int kStep = S::LW + S::LX + 1, kAhead = (EW > 0 ? S::LW : 0) + (ST - 1) * kStep;
+  // A step's loads: W, X, scales. kAhead may still be in flight when the first step's are needed.
+  constexpr int kStep = S::LW + S::LX + 1, kAhead = (ST - 1) * kStep;
   auto first_loads = [&]() {
-    if constexpr (EW > 0) load_w(begin, 0);
 #pragma unroll
     for (int i = 0; i < ST; ++i) {
-      load_x(min(begin + i, end - 1), i);
-      load_w(min(begin + i + EW, end - 1), i + EW);
+      const int step = min(begin + i, end - 1);
+      load_w(step, i, 0, S::LW);
+      load_x(step, i, 0, S::LX);
+      load_s(step, i);
     }
     wait_loads<kAhead>();
     __builtin_amdgcn_s_barrier();
   };
   // On to the next step: its loads have landed and every wave holds the rest of this one in registers, so this step's buffers
-  // are free for loads.
+  // are free for loads, of which `early` are under way.
+  constexpr bool STREAM = LARGE && !WIDE;
+  constexpr int kEarly = STREAM ? S::LW + S::LX / 2 : 0;
   auto next_step = [&](auto more) {
-    wait_loads<decltype(more)::value ? kAhead - kStep : 0>();
+    wait_loads<decltype(more)::value ? kAhead - kStep + kEarly : 0>();
     __builtin_amdgcn_s_barrier();
     if constexpr (decltype(more)::value) {
-      load_x(s + ST, xbuf);
-      load_w(min(s + ST + EW, end - 1), wbuf);
+      if constexpr (!STREAM) load_w(s + ST, buf, 0, S::LW);
+      load_x(s + ST, buf, STREAM ? S::LX / 2 : 0, S::LX);
+      load_s(s + ST, buf);
     }
-    advance();
+    buf = buf == (uint32_t)(ST - 1) ? 0u : buf + 1u;
     ++s;
   };
+  auto load_early = [&](int i) {
+    if (i < S::LW) load_w(s + ST, buf, i, i + 1);
+    else load_x(s + ST, buf, i - S::LW, i - S::LW + 1);
+  };
+  auto wait_lds = [&]() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); };
   using More = std::true_type;
   using Rest = std::false_type;
 
   // Large tiles: the layer's operands of a block stay in registers, those of the rows come one tile of 16 ahead, and the sums of a
-  // tile of 16 rows are added up while the matrix cores work on the next.
+  // tile of 16 rows are added up while the matrix cores work on the next. Once every wave holds the layer's operands and the first
+  // half of the rows', their buffers are filled again, a few loads with each of the row tiles that are left.
   auto stream_loop = [&](auto rows) __attribute__((always_inline)) {
     constexpr int R = decltype(rows)::value;
-    static_assert(U == 1 && R % 2 == 0, "");
+    static_assert(U == 1 && R % 2 == 0 && S::LX % 2 == 0, "");
+    constexpr int kMiddle = R == RX ? R / 2 - 1 : R - 1;   // row tiles of fewer lie in the first half all
     i32x8 w[AT], x[2];
     f32x4 p[2][AT];
     float xs[2], ws, before = 0.f;               // before: the scale of the sums in hand
@@ -240,11 +241,6 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
       constexpr bool LAST = decltype(last)::value;
       const int left = LAST ? a.n - s * BK : BK;
       if constexpr (LAST) cut(x[0], left);
-      Wide ww[WIDE ? AT : 1];
-      if constexpr (WIDE) {
-#pragma unroll
-        for (int t = 0; t < AT; ++t) ww[t] = widen_all(w[t]);
-      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const int cur = r & 1;
@@ -253,28 +249,28 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
           xs[cur ^ 1] = read_xs(r + 1, 0);
           x[cur ^ 1] = read_x(r + 1, 0);
           if constexpr (LAST) cut(x[cur ^ 1], left);
-        } else if constexpr (!LAST) {
+        }
+        if (decltype(more)::value && r == kMiddle) {
+          wait_lds();
+          __builtin_amdgcn_s_barrier();
+        }
+        if (decltype(more)::value && r >= kMiddle) {
+          constexpr int PER = (kEarly + R - kMiddle - 1) / (R - kMiddle);
+#pragma unroll
+          for (int e = (r - kMiddle) * PER; e < min(kEarly, (r - kMiddle + 1) * PER); ++e) load_early(e);
+        }
+        if (!LAST && r == R - 1) {
           next_step(more);
           read_first(last);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (WIDE) {
-          wide_products(p[cur], ww, widen_all(x[cur]));
 #pragma unroll
-          for (int t = 0; t < AT; ++t) {
-            add(acc[t][(r + R - 1) % R], p[cur ^ 1][t], before);
-            if (!LAST && r == R - 1) w[t] = read_w(t, 0);
-          }
-        } else {
-#pragma unroll
-          for (int t = 0; t < AT; ++t) {
-            p[cur][t] = product(w[t], x[cur]);
-            if (!LAST && r == R - 1) w[t] = read_w(t, 0);
-            add(acc[t][(r + R - 1) % R], p[cur ^ 1][t], before);
-            __builtin_amdgcn_sched_barrier(0);
-          }
+        for (int t = 0; t < AT; ++t) {
+          p[cur][t] = product(w[t], x[cur]);
+          if (!LAST && r == R - 1) w[t] = read_w(t, 0);
+          add(acc[t][(r + R - 1) % R], p[cur ^ 1][t], before);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
         before = scale;
       }
     };
@@ -285,14 +281,75 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
     for (int t = 0; t < AT; ++t) add(acc[t][R - 1], p[1][t], before);
   };
 
-  // Small tiles: the operands and scales of a block are read while the matrix cores work on the block before.
+  // Tiles of 32-bit outputs: the rows' operands of a block are widened at once and the layer's one by one, which leaves their places to
+  // the next block's.
+  auto wide_loop = [&](auto rows) __attribute__((always_inline)) {
+    constexpr int R = decltype(rows)::value;
+    static_assert(U == 1 && R % 2 == 0, "");
+    i32x8 w[AT], x[R];
+    float xs[R], ws;
+    auto read_rows = [&]() __attribute__((always_inline)) {
+      ws = read_ws(0);
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        xs[r] = read_xs(r, 0);
+        x[r] = read_x(r, 0);
+      }
+    };
+    first_loads();
+    read_rows();
+#pragma unroll
+    for (int t = 0; t < AT; ++t) w[t] = read_w(t, 0);
+    auto step = [&](auto last, auto more) __attribute__((always_inline)) {
+      constexpr bool LAST = decltype(last)::value;
+      const int left = LAST ? a.n - s * BK : BK;
+      Wide xw[R];
+      float scale[R];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if constexpr (LAST) cut(x[r], left);
+        scale[r] = xs[r] * ws;
+        xw[r] = widen_all(x[r]);
+      }
+#pragma unroll
+      for (int t = 0; t < AT; ++t) {
+        const Wide ww = widen_all(w[t]);
+        if constexpr (!LAST) {
+          if (t == 0) next_step(more);
+          w[t] = read_w(t, 0);
+          if (t == AT - 1) read_rows();
+        }
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {
+          f32x4 p[2];
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) p[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ww.q[q], xw[r + i].q[q], q == 0 ? zero : p[i], 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) add(acc[t][r + i], p[i], scale[r + i]);
+        }
+      }
+    };
+    while (s < end - ST) step(std::false_type{}, More{});
+    while (s < end - 1) step(std::false_type{}, Rest{});
+    step(std::true_type{}, Rest{});
+  };
+
+  // Small tiles: the operands and scales of a block are read, and the sums of the block before are added up, while the matrix cores
+  // work on a block.
   struct Frags {
     i32x8 w[AT], x[RX];
     float xs[RX], ws;
   };
+  struct Sums {
+    f32x4 p[AT][RX];
+    float scale[RX];
+  };
   auto ahead_loop = [&](auto rows) __attribute__((always_inline)) {
     constexpr int R = decltype(rows)::value;
     Frags f[2];
+    Sums z[2];
     auto read = [&](Frags& f, int u) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
@@ -303,37 +360,63 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
 #pragma unroll
       for (int t = 0; t < AT; ++t) f.w[t] = read_w(t, u);
     };
-    auto multiply = [&](const Frags& f) {
-      Wide ww[WIDE ? AT : 1];
+    auto multiply = [&](const Frags& f, Sums& z) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) z.scale[r] = f.xs[r] * f.ws;
       if constexpr (WIDE) {
+        constexpr int PAIR = R > 1 ? 2 : 1;      // row tiles whose chains of four products take turns
+        Wide w[AT];
 #pragma unroll
-        for (int t = 0; t < AT; ++t) ww[t] = widen_all(f.w[t]);
-      }
+        for (int t = 0; t < AT; ++t) w[t] = widen_all(f.w[t]);
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        f32x4 p[AT];
-        if constexpr (WIDE) {
-          wide_products(p, ww, widen_all(f.x[r]));
-        } else {
+        for (int r = 0; r < R; r += PAIR) {
+          Wide x[PAIR];
 #pragma unroll
-          for (int t = 0; t < AT; ++t) p[t] = product(f.w[t], f.x[r]);
+          for (int i = 0; i < PAIR; ++i) x[i] = widen_all(f.x[r + i]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int t = 0; t < AT; ++t)
+#pragma unroll
+              for (int i = 0; i < PAIR; ++i)
+                z.p[t][r + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[t].q[q], x[i].q[q], q == 0 ? zero : z.p[t][r + i], 0, 0, 0);
         }
+      } else {
 #pragma unroll
-        for (int t = 0; t < AT; ++t) add(acc[t][r], p[t], f.xs[r] * f.ws);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int t = 0; t < AT; ++t) z.p[t][r] = product(f.w[t], f.x[r]);
       }
     };
+    auto add_up = [&](const Sums& z) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < AT; ++t) add(acc[t][r], z.p[t][r], z.scale[r]);
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      z[1].scale[r] = 0.f;
+#pragma unroll
+      for (int t = 0; t < AT; ++t) z[1].p[t][r] = zero;
+    }
     first_loads();
     read(f[0], 0);
-    auto step = [&](auto more, auto first) __attribute__((always_inline)) {     // from set `first` on
+    auto step = [&](auto more, auto first) __attribute__((always_inline)) {   // from set `first` on
       constexpr int F = decltype(first)::value;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (u == U - 1) next_step(more);
         read(f[(F + u + 1) & 1], (u + 1) % U);
         __builtin_amdgcn_sched_barrier(0);
-        multiply(f[(F + u) & 1]);
+        multiply(f[(F + u) & 1], z[(F + u) & 1]);
+        add_up(z[(F + u + 1) & 1]);
         __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    auto back = [&]() {                          // an odd number of blocks: what is in hand goes to where an even one leaves it
+      f[0] = f[1];
+      z[1] = z[0];
     };
     using Even = std::integral_constant<int, 0>;
     using Odd = std::integral_constant<int, 1>;
@@ -346,13 +429,14 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
       }
       if (s < end - ST) {
         step(More{}, Even{});
-        f[0] = f[1];
+        back();
       }
     }
     while (s < end - 1) {
       step(Rest{}, Even{});
-      if constexpr (U % 2 == 1) f[0] = f[1];
+      if constexpr (U % 2 == 1) back();
     }
+    add_up(z[1]);
     const int left = a.n - s * BK;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -360,16 +444,18 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
       if (u < U - 1) read(f[(u + 1) & 1], u + 1);
 #pragma unroll
       for (int r = 0; r < R; ++r) cut(f[u & 1].x[r], left - 128 * u);
-      multiply(f[u & 1]);
+      multiply(f[u & 1], z[0]);
+      add_up(z[0]);
     }
   };
   auto main_loop = [&](auto rows) __attribute__((always_inline)) {
-    if constexpr (STREAM) stream_loop(rows);
+    if constexpr (LARGE && WIDE) wide_loop(rows);
+    else if constexpr (LARGE) stream_loop(rows);
     else ahead_loop(rows);
   };
   // The rows' tiles of 16 go round the waves, and a wave multiplies all of its own, half or a quarter, as the tile has rows.
   const int there = ((tile.count + 15) / 16 - wx + S::WX - 1) / S::WX;
-  constexpr int kLeast = STREAM ? 2 : 1;         // the streaming loop takes them in pairs
+  constexpr int kLeast = LARGE ? 2 : 1;          // an even number of products, and of rows' tiles widened together
   if constexpr (RX / 2 >= kLeast) {
     if (there > RX / 2) {
       main_loop(std::integral_constant<int, RX>{});
@@ -442,39 +528,63 @@ static hipError_t launch_shape_t(const Product8Args& a, hipStream_t s) {
 
 template <class S>
 static hipError_t launch_shape(const Product8Args& a, hipStream_t s) {
-  if (a.out == kF32) return launch_shape_t<S, kF32>(a, s);
+  if constexpr (S::AT * S::RX < 32) {
+    if (a.out == kF32) return launch_shape_t<S, kF32>(a, s);
+  }
   if (a.out == kF16) return launch_shape_t<S, kF16>(a, s);
   return launch_shape_t<S, kBf16>(a, s);
 }
 
-// The tile shapes. What one costs: microseconds per 128 bytes of the inner axis for a compute unit that holds one workgroup, and
-// for one that holds two; microseconds per tile beside that (its first loads, its stores).
-struct TileCost {
+// The tile shapes: outputs, rows, workgroups on a compute unit.
+struct TileSize {
   int out, rows, resident;
+};
+constexpr TileSize kTiles[] = {
+    {256, 256, 1},  // TileShape<4, 8, 4, 2, 128, 2>, not for 32-bit outputs: its registers do not hold widened operands
+    {256, 128, 1},  // TileShape<4, 4, 4, 2, 128, 3>
+    {128, 128, 2},  // TileShape<4, 4, 2, 2, 128, 2>
+    {128, 64, 2},   // TileShape<2, 4, 4, 1, 128, 3>
+    {64, 64, 2},    // TileShape<2, 2, 2, 2, 128, 4>
+    {64, 32, 2},    // TileShape<1, 2, 4, 1, 256, 3>
+    {64, 16, 2},    // TileShape<1, 1, 4, 1, 256, 3>
+    {32, 16, 2},    // TileShape<1, 1, 2, 1, 512, 3>
+};
+constexpr int kShapes = sizeof(kTiles) / sizeof(kTiles[0]);
+
+// What they cost with 16-bit and with 32-bit outputs, fitted to 14 layers (130 to 28672 outputs, 768 to 20000 inputs) at 1 to 4096
+// rows and 11 sets of experts: microseconds per 128 of the inner axis for a compute unit that holds one workgroup, and for one that
+// holds two; microseconds per tile beside that (its first loads, its stores). Of the product: bytes per microsecond where it
+// waits for memory alone, and the part of the shorter of the two times that the longer does not hide; of a split inner axis:
+// microseconds at all, for each part, and for each value of a part's sums.
+struct TileCost {
   float alone, shared, tile;
 };
-constexpr TileCost kTiles[] = {
-    {256, 256, 1, 1.484f, 1.484f, 5.05f}, // TileShape<4, 8, 4, 2, 128, 2>
-    {256, 128, 1, 0.974f, 0.974f, 4.26f}, // TileShape<4, 4, 4, 2, 128, 3>
-    {128, 128, 1, 0.533f, 0.533f, 2.24f}, // TileShape<2, 4, 4, 2, 128, 3>
-    {128, 64, 2, 0.321f, 0.677f, 2.28f},  // TileShape<2, 4, 4, 1, 128, 3>
-    {64, 32, 2, 0.124f, 0.222f, 1.13f},   // TileShape<1, 2, 4, 1, 256, 3>
-    {32, 16, 2, 0.047f, 0.14f, 0.85f},    // TileShape<1, 1, 2, 1, 512, 3>
+struct Costs {
+  TileCost tiles[kShapes];
+  float stream, unhidden, join, part, value;
 };
-constexpr float kStreamRate = 5.3e6f;   // bytes per microsecond of a product that waits for memory alone
+constexpr Costs kCosts[2] = {
+    {{{1.587f, 1.587f, 5.65f}, {0.988f, 0.988f, 3.33f}, {0.618f, 1.062f, 3.35f}, {0.459f, 0.748f, 2.65f},
+      {0.298f, 0.476f, 2.12f}, {0.168f, 0.326f, 1.91f}, {0.147f, 0.256f, 1.31f}, {0.084f, 0.132f, 2.57f}},
+     7.78e6f, 0.676f, 0.43f, 0.445f, 2.78e-6f},
+    {{{0.f, 0.f, 0.f}, {1.527f, 1.527f, 8.48f}, {0.972f, 1.723f, 5.37f}, {0.590f, 1.084f, 3.57f},
+      {0.384f, 0.668f, 2.49f}, {0.243f, 0.431f, 1.98f}, {0.192f, 0.322f, 1.42f}, {0.135f, 0.194f, 2.31f}},
+     6.39e6f, 0.348f, 0.08f, 0.384f, 2.14e-6f}};
 
-// The cheapest shape and split of the inner axis: rounds of workgroups over the compute units, and the time that the
-// bytes take, of which a part is not hidden behind the other. Experts: row tiles as an even routing fills them, one half-filled
-// for each expert.
-Int8Plan fp8_plan(int M, int m, int n, int experts) {
+// The cheapest shape and split of the inner axis: rounds of workgroups over the compute units, and the time that the bytes
+// take. Over the sweep this loses 1.5% against trying everything (37% at worst, 9 of 34 us). Experts: row tiles as an even routing
+// fills them, one half-filled for each expert; their inner axis stays whole, as their launch has no workspace.
+Int8Plan fp8_plan(int M, int m, int n, int experts, bool wide) {
+  const Costs& c = kCosts[wide ? 1 : 0];
   const float reached = experts > 0 ? (float)(experts < M ? experts : M) : 1.f;
   const float rows = (float)M / reached;
-  const float stream = (reached * m * (float)n + (float)M * n + 2.f * M * m) / kStreamRate;
+  const float stream = (reached * m * (float)n + (float)M * n + 2.f * M * m) / c.stream;
   const int steps = (n + 127) / 128;
   Int8Plan best{0, 1};
   float least = 3.0e38f;
-  for (int shape = 0; shape < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++shape) {
-    const TileCost& t = kTiles[shape];
+  for (int shape = wide ? 1 : 0; shape < kShapes; ++shape) {
+    const TileSize& t = kTiles[shape];
+    const TileCost& cost = c.tiles[shape];
     if (t.rows > 32 && t.rows > 2.f * rows) continue;          // more than half of it empty
     const float rt = experts > 0 ? reached * (rows / t.rows + 0.5f > 1.f ? rows / t.rows + 0.5f : 1.f)
                                  : (float)((M + t.rows - 1) / t.rows);
@@ -485,10 +595,10 @@ Int8Plan fp8_plan(int M, int m, int n, int experts) {
       const float groups = tiles * splits;
       const float rounds = (float)(int64_t)(groups / slots), rest = groups - rounds * slots;
       const float len = (float)((steps + splits - 1) / splits);
-      float work = rounds * (t.shared * len + t.tile);
-      if (rest > 0.f) work += (rest > kComputeUnits ? t.shared : t.alone) * len + t.tile;
-      float us = (work > stream ? work : stream) + 0.2f * (work > stream ? stream : work);
-      if (splits > 1) us += 0.9f + 2.1e-6f * splits * M * m;
+      float work = rounds * (cost.shared * len + cost.tile);
+      if (rest > 0.f) work += (rest > kComputeUnits ? cost.shared : cost.alone) * len + cost.tile;
+      float us = (work > stream ? work : stream) + c.unhidden * (work > stream ? stream : work);
+      if (splits > 1) us += c.join + c.part * splits + c.value * splits * M * m;
       if (us < least) {
         least = us;
         best = {shape, splits};
@@ -503,24 +613,31 @@ void fp8_plan_tile(const Int8Plan& p, int* outputs, int* rows) {
   *rows = kTiles[p.shape].rows;
 }
 
+// For outputs of every type.
 size_t fp8_partial_bytes(int M, int m, int n) {
-  const Int8Plan p = fp8_plan(M, m, n, 0);
-  if (p.splits <= 1) return 0;
-  const TileCost& t = kTiles[p.shape];
-  return (size_t)((m + t.out - 1) / t.out) * ((M + t.rows - 1) / t.rows) * p.splits * t.out * t.rows * 4;
+  size_t most = 0;
+  for (bool wide : {false, true}) {
+    const Int8Plan p = fp8_plan(M, m, n, 0, wide);
+    const TileSize& t = kTiles[p.shape];
+    const size_t bytes = (size_t)((m + t.out - 1) / t.out) * ((M + t.rows - 1) / t.rows) * p.splits * t.out * t.rows * 4;
+    if (p.splits > 1 && bytes > most) most = bytes;
+  }
+  return most;
 }
 
 hipError_t launch_fp8_gemm(const Product8Args& args, hipStream_t s) {
   Product8Args a = args;
-  const Int8Plan p = fp8_plan(a.M, a.m, a.n, a.offsets ? a.experts : 0);
+  const Int8Plan p = fp8_plan(a.M, a.m, a.n, a.offsets ? a.experts : 0, a.out == kF32);
   a.splits = p.splits;
   switch (p.shape) {
     case 0: return launch_shape<TileShape<4, 8, 4, 2, 128, 2>>(a, s);
     case 1: return launch_shape<TileShape<4, 4, 4, 2, 128, 3>>(a, s);
-    case 2: return launch_shape<TileShape<2, 4, 4, 2, 128, 3>>(a, s);
+    case 2: return launch_shape<TileShape<4, 4, 2, 2, 128, 2>>(a, s);
     case 3: return launch_shape<TileShape<2, 4, 4, 1, 128, 3>>(a, s);
-    case 4: return launch_shape<TileShape<1, 2, 4, 1, 256, 3>>(a, s);
-    case 5: return launch_shape<TileShape<1, 1, 2, 1, 512, 3>>(a, s);
+    case 4: return launch_shape<TileShape<2, 2, 2, 2, 128, 4>>(a, s);
+    case 5: return launch_shape<TileShape<1, 2, 4, 1, 256, 3>>(a, s);
+    case 6: return launch_shape<TileShape<1, 1, 4, 1, 256, 3>>(a, s);
+    case 7: return launch_shape<TileShape<1, 1, 2, 1, 512, 3>>(a, s);
     default: return hipErrorInvalidValue;
   }
 }

@@ -180,7 +180,7 @@ size_t int8_partial_bytes(int M, int m, int n);
 hipError_t launch_int8_quantize(int rows, int n, const void* x, int dtype, int64_t ldx, int8_t* q, int64_t ldq,
                                 float* scales, hipStream_t s);
 hipError_t launch_int8_gemm(const Product8Args& a, hipStream_t s);
-Int8Plan fp8_plan(int M, int m, int n, int experts);
+Int8Plan fp8_plan(int M, int m, int n, int experts, bool wide);   // wide: binary32 outputs
 void fp8_plan_tile(const Int8Plan& p, int* outputs, int* rows);
 size_t fp8_partial_bytes(int M, int m, int n);
 hipError_t launch_fp8_quantize(int rows, int n, const void* x, int dtype, int64_t ldx, bool layer, uint8_t* q, int64_t ldq,

@@ -578,14 +578,14 @@ int32_t tg_int8_plan(int32_t rows, int32_t m, int32_t n, int32_t experts, int32_
  * Root-mean-square norm of rows, with the residual's addition before it and a quantiser behind it (what stands in front
  * of every linear layer of a decoder: lecture, Part one):
  *     h = x + residual, summed in binary32 and rounded to the residual's type (x itself without a residual); h goes to total,
- *     r = 1 / sqrt(mean_i h_i^2 + eps), the sum in binary64,
+ *     r = 1 / sqrt(mean_i h_i^2 + eps), eight neighbouring squares summed in binary32 and those sums in binary64,
  *     y_i = h_i * w_i * r                                          out_dtype TG_F32, TG_F16, TG_BF16
  *     amax = max_i |h_i w_i|, q_i = the whole number nearest to 127 h_i w_i / amax (an exact half to the even one),
  *            scale = amax * r / 127                                out_dtype TG_INT8: what int8_gemm reads
  *     amax over each 128 neighbours (fewer at the row's end), q_i = the e4m3 value nearest to 448 h_i w_i / amax (ties to the
  *            even code), scale = amax * r / 448                    out_dtype TG_E4M3: what fp8_gemm reads
  * The norm scales a row as a whole, so the steps q do not depend on it; they are decided exactly, on exact products h_i w_i.
- * y and the scales are rounded from binary64. A row of zeros gives zeros. A row with a NaN or an infinity in h gives NaN, in
+ * A scale is rounded once, y in binary32 and once more to a 16-bit type. A row of zeros gives zeros. A row with a NaN or an infinity in h gives NaN, in
  * 8 bits zeros with NaN scales; a NaN or an infinity in w only its own y_i, or the scale of its row or 128 values.
  *   rows : 1 .. 2^24; n : 1 .. 32768.
  *   x        : device, rows of n values of type dtype, row stride ldx >= n elements.

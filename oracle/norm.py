@@ -16,10 +16,11 @@ from . import fp8
 def round_to(v, kind):
     """float64 values rounded to "float32", "float16" or "bfloat16", halves to even."""
     v = np.asarray(v, np.float64)
-    if kind == "float32":
-        return v.astype(np.float32).astype(np.float64)
-    if kind == "float16":
-        return v.astype(np.float16).astype(np.float64)
+    with np.errstate(over="ignore"):
+        if kind == "float32":
+            return v.astype(np.float32).astype(np.float64)
+        if kind == "float16":
+            return v.astype(np.float16).astype(np.float64)
     fine = np.isfinite(v) & (v != 0)
     e = np.frexp(np.where(fine, v, 1.0))[1] - 1
     step = np.ldexp(1.0, np.maximum(e, -126) - 7)

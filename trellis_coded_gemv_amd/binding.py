@@ -752,24 +752,15 @@ def _blocks(n: int) -> int:
     return (n + _FP8_BLOCK - 1) // _FP8_BLOCK
 
 
-def _rows_of(x):
-    """x [..., n] as rows with neighbouring values: (rows, n, the tensor that holds them, their stride)."""
-    n = x.shape[-1]
-    x2 = x if x.dim() == 2 else x.reshape(-1, n)
-    if x2.stride(1) != 1 and n > 1:
-        x2 = x2.contiguous()
-    rows = x2.shape[0]
-    return rows, n, x2, (x2.stride(0) if rows > 1 else n)
+_OUT_TYPES = {}          # out_dtype of rms_norm -> its code in the C entry point
 
 
-def _rows_out(where: str, name: str, t, shape, dtype, device):
-    """A caller's output, checked, or a new one: (tensor, row stride)."""
-    if t is None:
-        return _torch().empty(shape, dtype=dtype, device=device), shape[-1]
+def _given_rows(where: str, name: str, t, shape, dtype) -> int:
+    """Row stride of a caller's output, which has to be of this shape and type with neighbouring values in a row."""
     _expect(t.dtype == dtype and t.shape == shape, where, f"expected {name} {dtype} {tuple(shape)}")
-    _expect(t.is_contiguous() or (t.dim() == 2 and (t.stride(1) == 1 or shape[1] == 1) and (t.stride(0) >= shape[1] or shape[0] == 1)), where,
-            f"expected {name} with neighbouring values")
-    return t, (t.stride(0) if t.dim() == 2 and shape[0] > 1 else shape[-1])
+    rows_apart = t.dim() == 2 and (t.stride(1) == 1 or shape[1] == 1) and (t.stride(0) >= shape[1] or shape[0] == 1)
+    _expect(rows_apart or t.is_contiguous(), where, f"expected {name} with neighbouring values")
+    return t.stride(0) if t.dim() == 2 and shape[0] > 1 else shape[-1]
 
 
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, total=None, y=None, scales=None, stream=None):
@@ -781,56 +772,82 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, total=
     torch = _torch()
     w = "rms_norm"
     dtype = _dtype_code(x.dtype, w)
-    out_dtype = out_dtype or (x.dtype if y is None else y.dtype)
-    out = {torch.int8: 3, torch.float8_e4m3fn: 4}.get(out_dtype)
+    if not _OUT_TYPES:
+        _OUT_TYPES.update(_DTYPES)
+        _OUT_TYPES.update({torch.int8: 3, torch.float8_e4m3fn: 4})
+    if out_dtype is None:
+        out_dtype = x.dtype if y is None else y.dtype
+    out = _OUT_TYPES.get(out_dtype)
     if out is None:
-        out = _dtype_code(out_dtype, w)
+        raise ValueError(f"{w}: expected out_dtype float32, float16, bfloat16, int8 or float8_e4m3fn, got {out_dtype}")
     shape = x.shape
-    if len(shape) < 1 or x.numel() == 0:
+    size = x.numel()
+    if len(shape) < 1 or size == 0:
         raise ValueError(f"{w}: expected rows [..., n]")
-    if (x.numel() // shape[-1] | shape[-1]) >> 31:
+    n = shape[-1]
+    rows = size // n
+    if (rows | n) >> 31:
         raise TgError(-2, w)
-    _expect(weight.shape == shape[-1:] and weight.is_contiguous(), w, f"expected a contiguous weight [{shape[-1]}]")
     wtype = _dtype_code(weight.dtype, w)
-    rtype = 0
+    if weight.shape != (n,) or not weight.is_contiguous():
+        raise ValueError(f"{w}: expected a contiguous weight [{n}]")
     if residual is not None:
         rtype = _dtype_code(residual.dtype, w)
-        _expect(residual.shape == shape, w, f"expected a residual {tuple(shape)}")
-    else:
-        _expect(total is None, w, "total without a residual")
+        if residual.shape != shape:
+            raise ValueError(f"{w}: expected a residual {tuple(shape)}")
+    elif total is not None:
+        raise ValueError(f"{w}: total without a residual")
     at = _common_device(w, x, weight, residual, total, y, scales)
     if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
             return rms_norm(x, weight, residual, eps, out_dtype, total, y, scales)
-    rows, n, x2, ldx = _rows_of(x)
-    r2, ldr, ldt = None, n, n
+    device, flat = x.device, len(shape) == 2
+    x2 = x if flat else x.reshape(rows, n)
+    ldx, inner = x2.stride()
+    if inner != 1 and n > 1:
+        x2, ldx = x2.contiguous(), n
+    r, t, ldr, ldt = None, None, n, n
     if residual is not None:
-        _, _, r2, ldr = _rows_of(residual)
-        total, ldt = _rows_out(w, "total", total, shape, residual.dtype, x.device)
-    y, ldy = _rows_out(w, "y", y, shape, out_dtype, x.device)
-    lds = 0
-    if out == 4:
-        scales, lds = _rows_out(w, "scales", scales, shape[:-1] + (_blocks(n),), torch.float32, x.device)
-    elif out == 3:
-        scales, lds = _row_scales(w, scales, shape[:-1], x.device), 1
+        r2 = residual if flat else residual.reshape(rows, n)
+        ldr, inner = r2.stride()
+        if inner != 1 and n > 1:
+            r2, ldr = r2.contiguous(), n
+        if total is None:
+            total = torch.empty(rows, n, dtype=residual.dtype, device=device)   # numbers: a shape takes twice as long
+            total = total if flat else total.view(shape)
+        else:
+            ldt = _given_rows(w, "total", total, shape, residual.dtype)
+        r, t = r2.data_ptr(), total.data_ptr()
     else:
+        rtype = 0
+    if y is None:
+        y, ldy = torch.empty(rows, n, dtype=out_dtype, device=device), n
+        y = y if flat else y.view(shape)
+    else:
+        ldy = _given_rows(w, "y", y, shape, out_dtype)
+    lds = 1
+    if out < 3:
         _expect(scales is None, w, "scales without 8-bit outputs")
-    status = (_lib or lib()).rms_norm(rows, n, x2.data_ptr(), dtype, ldx, None if r2 is None else r2.data_ptr(), rtype, ldr,
-                                      None if total is None else total.data_ptr(), ldt, weight.data_ptr(), wtype, eps, y.data_ptr(), out, ldy,
-                                      None if scales is None else scales.data_ptr(), lds, torch._C._cuda_getCurrentRawStream(at))
+    elif scales is None:
+        if out == 4:
+            lds = (n + 127) >> 7
+            scales = torch.empty(rows, lds, dtype=torch.float32, device=device)
+            scales = scales if flat else scales.view(shape[:-1] + (lds,))
+        else:
+            scales = torch.empty(rows, dtype=torch.float32, device=device)
+            scales = scales if flat else scales.view(shape[:-1])
+    elif out == 4:
+        lds = _given_rows(w, "scales", scales, shape[:-1] + (_blocks(n),), torch.float32)
+    else:
+        _expect(scales.dtype == torch.float32 and scales.shape == shape[:-1] and scales.is_contiguous(), w, "expected a float32 scale for each row")
+    status = (_lib or lib()).rms_norm(rows, n, x2.data_ptr(), dtype, ldx if rows > 1 else n, r, rtype, ldr if rows > 1 else n, t, ldt,
+                                      weight.data_ptr(), wtype, eps, y.data_ptr(), out, ldy, None if scales is None else scales.data_ptr(), lds,
+                                      torch._C._cuda_getCurrentRawStream(at))
     if status:
         raise TgError(status, w)
-    got = (y,) if out < 3 else (y, scales)
-    if residual is not None:
-        got += (total,)
-    return got if len(got) > 1 else y
-
-
-def _row_scales(where: str, scales, lead, device):
-    if scales is None:
-        return _torch().empty(lead, dtype=_torch().float32, device=device)
-    _expect(scales.dtype == _torch().float32 and scales.shape == lead and scales.is_contiguous(), where, "expected a float32 scale for each row")
-    return scales
+    if residual is None:
+        return y if scales is None else (y, scales)
+    return (y, total) if scales is None else (y, scales, total)
 
 
 def fp8_quantize(x, q=None, scales=None, block_rows: int = 1, stream=None):
@@ -841,20 +858,36 @@ def fp8_quantize(x, q=None, scales=None, block_rows: int = 1, stream=None):
     w = "fp8_quantize"
     dtype = _dtype_code(x.dtype, w)
     shape = x.shape
-    if len(shape) < 1 or x.numel() == 0:
+    size = x.numel()
+    if len(shape) < 1 or size == 0:
         raise ValueError(f"{w}: expected rows [..., n]")
-    _expect(block_rows == 1 or (block_rows == _FP8_BLOCK and len(shape) == 2), w, "block_rows is 1, or 128 of x [m, n]")
-    if (x.numel() // shape[-1] | shape[-1]) >> 31:
+    if block_rows != 1 and (block_rows != _FP8_BLOCK or len(shape) != 2):
+        raise ValueError(f"{w}: block_rows is 1, or 128 of x [m, n]")
+    n = shape[-1]
+    rows = size // n
+    if (rows | n) >> 31:
         raise TgError(-2, w)
     at = _common_device(w, x, q, scales)
     if stream is not None or at != torch._C._cuda_getDevice():
         with _Entered(at, stream):
             return fp8_quantize(x, q, scales, block_rows)
-    rows, n, x2, ldx = _rows_of(x)
-    q, ldq = _rows_out(w, "q", q, shape, torch.float8_e4m3fn, x.device)
-    lead = shape[:-1] if block_rows == 1 else (_blocks(rows),)
-    scales, lds = _rows_out(w, "scales", scales, lead + (_blocks(n),), torch.float32, x.device)
-    status = (_lib or lib()).fp8_quantize(rows, n, x2.data_ptr(), dtype, ldx, block_rows, q.data_ptr(), ldq, scales.data_ptr(), lds,
+    flat = len(shape) == 2
+    x2 = x if flat else x.reshape(rows, n)
+    ldx, inner = x2.stride()
+    if inner != 1 and n > 1:
+        x2, ldx = x2.contiguous(), n
+    if q is None:
+        q, ldq = torch.empty(rows, n, dtype=torch.float8_e4m3fn, device=x.device), n
+        q = q if flat else q.view(shape)
+    else:
+        ldq = _given_rows(w, "q", q, shape, torch.float8_e4m3fn)
+    lds, lines = (n + 127) >> 7, rows if block_rows == 1 else _blocks(rows)
+    if scales is None:
+        scales = torch.empty(lines, lds, dtype=torch.float32, device=x.device)
+        scales = scales if flat else scales.view(shape[:-1] + (lds,))
+    else:
+        lds = _given_rows(w, "scales", scales, (lines, lds) if flat else shape[:-1] + (lds,), torch.float32)
+    status = (_lib or lib()).fp8_quantize(rows, n, x2.data_ptr(), dtype, ldx if rows > 1 else n, block_rows, q.data_ptr(), ldq, scales.data_ptr(), lds,
                                           torch._C._cuda_getCurrentRawStream(at))
     if status:
         raise TgError(status, w)
@@ -925,10 +958,13 @@ def _fp8_rows(torch, where: str, n: int, xq, xs):
     ldx, inner = xq.stride()
     if width != n or inner != 1:
         raise ValueError(f"{where}: expected xq float8_e4m3fn [rows, {n}] with neighbouring values")
-    blocks = _blocks(n)
-    if xs.dtype != torch.float32 or xs.shape != (rows, blocks) or (xs.stride(1) != 1 and blocks > 1):
-        raise ValueError(f"{where}: expected float32 scales [rows, {blocks}] of xq, a row's neighbouring")
-    return rows, (ldx if rows > 1 else n), (xs.stride(0) if rows > 1 else blocks)
+    blocks = (n + 127) >> 7
+    if xs.dtype != torch.float32 or xs.shape != (rows, blocks):
+        raise ValueError(f"{where}: expected float32 scales [rows, {blocks}] of xq")
+    lds, inner = xs.stride()
+    if inner != 1 and blocks > 1:
+        raise ValueError(f"{where}: expected scales with neighbouring values in a row")
+    return rows, (ldx if rows > 1 else n), (lds if rows > 1 else blocks)
 
 
 def fp8_gemm(layer: "Fp8Layer", xq, xs, Y=None, out_dtype=None, ws=None, stream=None):

@@ -47,180 +47,277 @@ __device__ __forceinline__ double wave_max(double v) {
   return fmax(v, __shfl_xor(v, 32, 64));
 }
 
-// Eight values rounded to a 16-bit type.
-template <int DT>
-__device__ __forceinline__ void round8(float (&v)[8]) {
-  Raw8 r{};
+// Eight values as bits of a type; those of 16-bit types are rounded.
+__device__ __forceinline__ void widen(const Raw8& r, int type, float (&v)[8]) {
+  with_type(type, [&](auto t) { widen8<decltype(t)::value>(r, v); });
+}
+
+template <bool NARROW>
+__device__ __forceinline__ void narrow(const float (&v)[8], int type, Raw8& r) {
+  if (!NARROW && type == kF32) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r.a[i] = half_bits<DT>(v[2 * i]) | half_bits<DT>(v[2 * i + 1]) << 16;
-  widen8<DT>(r, v);
+    for (int i = 0; i < 4; ++i) {
+      r.a[i] = __builtin_bit_cast(uint32_t, v[i]);
+      r.b[i] = __builtin_bit_cast(uint32_t, v[i + 4]);
+    }
+  } else if (type == kF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.a[i] = half_bits<kF16>(v[2 * i]) | half_bits<kF16>(v[2 * i + 1]) << 16;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.a[i] = half_bits<kBf16>(v[2 * i]) | half_bits<kBf16>(v[2 * i + 1]) << 16;
+  }
+}
+
+// The first `valid` of eight values to a row.
+template <bool NARROW, bool TAIL>
+__device__ __forceinline__ void store8(const Raw8& r, int type, void* p, int64_t at, int valid) {
+  if (!NARROW && type == kF32) {
+    float* f = reinterpret_cast<float*>(p) + at;
+    if (!TAIL || valid >= 8) {
+      *reinterpret_cast<u32x4_any*>(f) = r.a;
+      *reinterpret_cast<u32x4_any*>(f + 4) = r.b;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < valid) f[i] = __builtin_bit_cast(float, (uint32_t)r.a[i]);
+        if (i + 4 < valid) f[i + 4] = __builtin_bit_cast(float, (uint32_t)r.b[i]);
+      }
+    }
+  } else {
+    uint16_t* h = reinterpret_cast<uint16_t*>(p) + at;
+    if (!TAIL || valid >= 8) {
+      *reinterpret_cast<u32x4_any*>(h) = r.a;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < valid) h[i] = (uint16_t)(r.a[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+
+// The pieces of a thread: `type` asks for the loads of all of them before any is looked at.
+template <int PER, bool NARROW, bool TAIL, class At>
+__device__ __forceinline__ void load_pieces(Raw8 (&raw)[PER], const void* p, int64_t row, int type, int n, At at) {
+  auto all = [&](auto t) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) load8<decltype(t)::value, TAIL>(raw[i], p, row + min(at(i), n - 1), n - at(i));
+  };
+  if (!NARROW && type == kF32) all(std::integral_constant<int, kF32>{});
+  else all(std::integral_constant<int, kF16>{});           // 16-bit types load alike
 }
 
 }  // namespace
 
-// A row is a workgroup's, in registers from its one read to its one write: piece c of eight values to thread c % THREADS, PER
-// pieces to a thread, so that 16 neighbouring lanes hold 128 neighbouring values.
-template <int THREADS, int PER>
+// A row is a workgroup's, in registers from its one read to its one write, as bits of the type that it is stored in: piece c of eight
+// values to thread c % THREADS, PER pieces to a thread, so that 16 neighbouring lanes hold 128 neighbouring values. NARROW: x, residual
+// and weight are of 16 bits. TAIL: rows end inside a piece.
+template <int THREADS, int PER, bool NARROW, bool TAIL>
 __global__ __launch_bounds__(THREADS) void rms_norm_kernel(const NormArgs a) {
-  __shared__ double sums[THREADS / 64], tops[THREADS / 64];
+  __shared__ double sums[THREADS / 64];
+  __shared__ uint32_t words[THREADS / 64];
   const int row = blockIdx.y * gridDim.x + blockIdx.x;
   if (row >= a.rows) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   auto at = [&](int i) { return 8 * ((int)threadIdx.x + THREADS * i); };   // first value of the thread's piece i
-  Raw8 xr[PER], rr[PER], wr[PER];
-  with_type(a.x_type, [&](auto t) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) load8<decltype(t)::value>(xr[i], a.x, (int64_t)row * a.ldx + min(at(i), a.n - 1), a.n - at(i));
-  });
-  if (a.residual) {
-    with_type(a.r_type, [&](auto t) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) load8<decltype(t)::value>(rr[i], a.residual, (int64_t)row * a.ldr + min(at(i), a.n - 1), a.n - at(i));
-    });
-  }
-  with_type(a.w_type, [&](auto t) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) load8<decltype(t)::value>(wr[i], a.w, min(at(i), a.n - 1), a.n - at(i));
-  });
+  Raw8 hr[PER], rr[PER], wr[PER];
+  load_pieces<PER, NARROW, TAIL>(hr, a.x, (int64_t)row * a.ldx, a.x_type, a.n, at);
+  if (a.residual) load_pieces<PER, NARROW, TAIL>(rr, a.residual, (int64_t)row * a.ldr, a.r_type, a.n, at);
+  load_pieces<PER, NARROW, TAIL>(wr, a.w, 0, a.w_type, a.n, at);
 
-  float h[PER][8];
-  with_type(a.x_type, [&](auto t) {
+  // Eight squares are summed in binary32, which eight roundings leave off by 8 * 2^-24 of their sum at most, and those sums in binary64;
+  // where squares may leave binary32's range, all in binary64.
+  const int h_type = a.residual ? a.r_type : a.x_type;
+  double sum = 0.0;
+  uint32_t top = 0;                              // int8: bits of the largest product, rounded to binary32
 #pragma unroll
-    for (int i = 0; i < PER; ++i) widen8<decltype(t)::value>(xr[i], h[i]);
-  });
-  if (a.residual) {
-    with_type(a.r_type, [&](auto t) {
-      constexpr int DT = decltype(t)::value;
+  for (int i = 0; i < PER; ++i) {
+    float h[8];
+    widen(hr[i], a.x_type, h);
+    if (a.residual) {
+      float r[8];
+      widen(rr[i], a.r_type, r);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        float r[8];
-        widen8<DT>(rr[i], r);
+      for (int e = 0; e < 8; ++e) h[e] += r[e];
+      narrow<NARROW>(h, a.r_type, hr[i]);
+      if (at(i) < a.n) store8<NARROW, TAIL>(hr[i], a.r_type, a.total, (int64_t)row * a.ldt + at(i), a.n - at(i));
+      widen(hr[i], a.r_type, h);
+    }
+    float part = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] += r[e];
-        if constexpr (DT != kF32) round8<DT>(h[i]);
-        if (at(i) < a.n) store_outputs<DT, 8>(a.total, (int64_t)row * a.ldt + at(i), h[i], a.n - at(i));
-      }
-    });
+    for (int e = 0; e < 8; ++e) part = fmaf(h[e], h[e], part);
+    if (part >= 0x1p-90f && part <= 0x1p100f) {
+      sum += (double)part;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum = fma((double)h[e], (double)h[e], sum);
+    }
+    if (a.out == kInt8) {
+      float w[8];
+      widen(wr[i], a.w_type, w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, __builtin_bit_cast(uint32_t, h[e] * w[e]) & 0x7FFFFFFFu);
+    }
   }
-
-  double sum = 0.0, top = 0.0;
-  uint32_t word = 0;
-  float w[PER][8];
-  with_type(a.w_type, [&](auto t) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) widen8<decltype(t)::value>(wr[i], w[i]);
-  });
-#pragma unroll
-  for (int i = 0; i < PER; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum = fma((double)h[i][e], (double)h[i][e], sum);
   if (a.out == kInt8) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double p = (double)h[i][e] * (double)w[i][e];
-        top = fmax(top, fabs(p));
-        word = max(word, magnitude_word(p));
-      }
-    if (word >= kNotFinite) top = __builtin_inf();
-    top = wave_max(top);
+    top = row16_max(top);
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
   }
   sum = wave_sum(sum);
   if constexpr (THREADS > 64) {
     if (lane == 0) {
       sums[wave] = sum;
-      tops[wave] = top;
+      words[wave] = top;
     }
     __syncthreads();
     sum = 0.0;
 #pragma unroll
     for (int v = 0; v < THREADS / 64; ++v) {
       sum += sums[v];
-      top = fmax(top, tops[v]);
+      top = max(top, words[v]);
     }
   }
   const bool finite = sum < __builtin_inf();     // a square of finite binary32 values is far from the end of binary64
   const double mean = sum / (double)a.n + (double)a.eps;
   const double r = !finite ? __builtin_nan("") : mean > 0.0 ? 1.0 / sqrt(mean) : 0.0;
 
+  // int8: the row's largest product. It is what binary32 says of products of 16-bit values in its range; of wider ones, it is the
+  // largest of those that are rounded to what binary32 says; out of its range, the largest of all in binary64 (every thread alike).
+  double most = 0.0, inv = 0.0;
+  bool good = finite, plain = false;
   if (a.out == kInt8) {
-    const bool good = finite && top < __builtin_inf();
-    const double inv = good && top > 0.0 ? 127.0 / top : 0.0;
-    if (threadIdx.x == 0) a.scales[(int64_t)row * a.lds] = good ? (float)(top * r / 127.0) : __builtin_nanf("");
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int valid = a.n - at(i);
-      if (valid <= 0) break;
-      uint32_t b[2] = {0, 0};
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        b[e >> 2] |= ((uint32_t)(good ? int8_step((double)h[i][e] * (double)w[i][e], inv, top) : 0) & 255u) << (8 * (e & 3));
-      uint8_t* q = reinterpret_cast<uint8_t*>(a.y) + (int64_t)row * a.ldy + at(i);
-      if (valid >= 8) {
-        *reinterpret_cast<u32x2_any*>(q) = u32x2_any{b[0], b[1]};
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < valid) q[e] = (uint8_t)(b[e >> 2] >> (8 * (e & 3)));
-      }
-    }
-  } else if (a.out == kE4m3) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      double p[2][4], most = 0.0;
-      uint32_t hi = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        p[e >> 2][e & 3] = (double)h[i][e] * (double)w[i][e];
-        most = fmax(most, fabs(p[e >> 2][e & 3]));
-        hi = max(hi, magnitude_word(p[e >> 2][e & 3]));
-      }
-      most = row16_max(most);
-      const bool good = finite && row16_max(hi) < kNotFinite;
-      const int valid = a.n - at(i);
-      if (valid <= 0) break;
-      if ((lane & 15) == 0) a.scales[(int64_t)row * a.lds + (at(i) >> 7)] = good ? (float)(most * r / (double)kE4m3Max) : __builtin_nanf("");
-      const double inv = good && most > 0.0 ? (double)kE4m3Max / most : 0.0;
-      uint32_t b[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) b[k] = good ? e4m3_steps(p[k], inv, most) : 0u;
-      uint8_t* q = reinterpret_cast<uint8_t*>(a.y) + (int64_t)row * a.ldy + at(i);
-      if (valid >= 8) {
-        *reinterpret_cast<u32x2_any*>(q) = u32x2_any{b[0], b[1]};
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < valid) q[e] = (uint8_t)(b[e >> 2] >> (8 * (e & 3)));
-      }
-    }
-  } else {
-    with_type(a.out, [&](auto t) {
+    plain = top >= 0x0D800000u && top <= 0x71800000u;   // 2^-100 to 2^100
+    most = (double)__builtin_bit_cast(float, top);
+    if (!NARROW || !plain) {
+      most = 0.0;
+      uint32_t word = 0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        float y[8];
+        float h[8], w[8];
+        widen(hr[i], h_type, h);
+        widen(wr[i], a.w_type, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = (float)((double)h[i][e] * (double)w[i][e] * r);
-        if (at(i) < a.n) store_outputs<decltype(t)::value, 8>(a.y, (int64_t)row * a.ldy + at(i), y, a.n - at(i));
+        for (int e = 0; e < 8; ++e)
+          if (!plain || (__builtin_bit_cast(uint32_t, h[e] * w[e]) & 0x7FFFFFFFu) == top) {
+            const double p = (double)h[e] * (double)w[e];
+            most = fmax(most, fabs(p));
+            word = max(word, magnitude_word(p));
+          }
       }
-    });
+      if (word >= kNotFinite) most = __builtin_inf();
+      most = wave_max(most);
+      if constexpr (THREADS > 64) {
+        __syncthreads();                         // every thread has read the sums
+        if (lane == 0) sums[wave] = most;
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < THREADS / 64; ++v) most = fmax(most, sums[v]);
+      }
+    }
+    good = finite && most < __builtin_inf();
+    inv = good && most > 0.0 ? 127.0 / most : 0.0;
+    if (threadIdx.x == 0) a.scales[(int64_t)row * a.lds] = good ? (float)(most * r / 127.0) : __builtin_nanf("");
+  }
+  const float inv32 = (float)inv;
+  const double step = r / (double)kE4m3Max;
+  const float r32 = (float)r;
+  const bool in_range = r >= 0x1p-120 && r <= 0x1p120;   // so h r32 is a normal number, or nothing beside the row's others
+
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    float h[8], w[8];
+    widen(hr[i], h_type, h);
+    widen(wr[i], a.w_type, w);
+    const int valid = a.n - at(i);
+    const int64_t to = (int64_t)row * a.ldy + at(i);
+    if (a.out == kE4m3) {
+      float v[2][4];
+      uint32_t bits = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        v[e >> 2][e & 3] = h[e] * w[e];
+        bits = max(bits, __builtin_bit_cast(uint32_t, v[e >> 2][e & 3]) & 0x7FFFFFFFu);
+      }
+      bits = row16_max(bits);
+      const BlockFactors f = block_factors(__builtin_bit_cast(float, bits));
+      double largest = (double)__builtin_bit_cast(float, bits);
+      bool fine = finite && bits < 0x7F800000u;
+      if (!NARROW || !f.plain) {                 // as for int8, in the 16 lanes of the block
+        double top64 = 0.0;
+        uint32_t word = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!f.plain || (__builtin_bit_cast(uint32_t, v[e >> 2][e & 3]) & 0x7FFFFFFFu) == bits) {
+            const double p = (double)h[e] * (double)w[e];
+            top64 = fmax(top64, fabs(p));
+            word = max(word, magnitude_word(p));
+          }
+        largest = row16_max(top64);
+        fine = finite && row16_max(word) < kNotFinite;
+      }
+      if (valid <= 0) break;
+      if ((lane & 15) == 0) a.scales[(int64_t)row * a.lds + (at(i) >> 7)] = fine ? (float)(largest * step) : __builtin_nanf("");
+      uint32_t b[2] = {0, 0};
+      if (fine) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          double p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = (double)h[4 * k + e] * (double)w[4 * k + e];
+          b[k] = e4m3_steps(v[k], p, f, largest);
+        }
+      }
+      store_bytes<TAIL>(reinterpret_cast<uint8_t*>(a.y) + to, b, valid);
+    } else if (a.out == kInt8) {
+      if (valid <= 0) break;
+      uint32_t b[2] = {0, 0};
+      if (good) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float t = h[e] * w[e] * inv32, k = rintf(t);
+          // t is off by 3 * 2^-24 of itself at most, less than 2^-15
+          int q = (int)k;
+          if (!plain || fabsf(fabsf(t - k) - 0.5f) <= 0x1p-14f) q = int8_step((double)h[e] * (double)w[e], inv, most);
+          b[e >> 2] |= ((uint32_t)q & 255u) << (8 * (e & 3));
+        }
+      }
+      store_bytes<TAIL>(reinterpret_cast<uint8_t*>(a.y) + to, b, valid);
+    } else {
+      if (valid <= 0) break;
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = in_range ? h[e] * r32 * w[e] : (float)((double)h[e] * (double)w[e] * r);
+      Raw8 bits;
+      narrow<false>(y, a.out, bits);
+      store8<false, TAIL>(bits, a.out, a.y, to, valid);
+    }
   }
 }
 
-// A row is a wave's up to 1024 values, and of 256 threads where a thread then holds one piece, or up to four of many rows, else
-// of 1024.
-hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+template <bool NARROW, bool TAIL>
+static void launch_norm(const NormArgs& a, hipStream_t s) {
   const int pieces = (a.n + 7) / 8;
   const unsigned x = a.rows < 65536 ? (unsigned)a.rows : 65536u;
   const dim3 grid(x, ((unsigned)a.rows + x - 1) / x);
-  if (pieces <= 64) hipLaunchKernelGGL((rms_norm_kernel<64, 1>), grid, dim3(64), 0, s, a);
-  else if (pieces <= 128) hipLaunchKernelGGL((rms_norm_kernel<64, 2>), grid, dim3(64), 0, s, a);
-  else if (pieces <= 256) hipLaunchKernelGGL((rms_norm_kernel<256, 1>), grid, dim3(256), 0, s, a);
-  else if (pieces <= 512 && a.rows >= 512) hipLaunchKernelGGL((rms_norm_kernel<256, 2>), grid, dim3(256), 0, s, a);
-  else if (pieces <= 1024 && a.rows >= 512) hipLaunchKernelGGL((rms_norm_kernel<256, 4>), grid, dim3(256), 0, s, a);
-  else if (pieces <= 1024) hipLaunchKernelGGL((rms_norm_kernel<1024, 1>), grid, dim3(1024), 0, s, a);
-  else if (pieces <= 2048) hipLaunchKernelGGL((rms_norm_kernel<1024, 2>), grid, dim3(1024), 0, s, a);
-  else hipLaunchKernelGGL((rms_norm_kernel<1024, 4>), grid, dim3(1024), 0, s, a);
+  // A row is a wave's up to 1024 values, and of 256 threads where a thread then holds one piece, or up to four of many rows, else
+  // of 1024.
+  const bool many = a.rows >= 512;
+  if (pieces <= 64) hipLaunchKernelGGL((rms_norm_kernel<64, 1, NARROW, TAIL>), grid, dim3(64), 0, s, a);
+  else if (pieces <= 128) hipLaunchKernelGGL((rms_norm_kernel<64, 2, NARROW, TAIL>), grid, dim3(64), 0, s, a);
+  else if (pieces <= 256) hipLaunchKernelGGL((rms_norm_kernel<256, 1, NARROW, TAIL>), grid, dim3(256), 0, s, a);
+  else if (pieces <= 512 && many) hipLaunchKernelGGL((rms_norm_kernel<256, 2, NARROW, TAIL>), grid, dim3(256), 0, s, a);
+  else if (pieces <= 768 && many) hipLaunchKernelGGL((rms_norm_kernel<256, 3, NARROW, TAIL>), grid, dim3(256), 0, s, a);
+  else if (pieces <= 1024 && many) hipLaunchKernelGGL((rms_norm_kernel<256, 4, NARROW, TAIL>), grid, dim3(256), 0, s, a);
+  else if (pieces <= 1024) hipLaunchKernelGGL((rms_norm_kernel<1024, 1, NARROW, TAIL>), grid, dim3(1024), 0, s, a);
+  else if (pieces <= 2048) hipLaunchKernelGGL((rms_norm_kernel<1024, 2, NARROW, TAIL>), grid, dim3(1024), 0, s, a);
+  else hipLaunchKernelGGL((rms_norm_kernel<1024, 4, NARROW, TAIL>), grid, dim3(1024), 0, s, a);
+}
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t s) {
+  const bool narrow = a.x_type != kF32 && a.w_type != kF32 && (!a.residual || a.r_type != kF32), tail = a.n % 8 != 0;
+  if (narrow) tail ? launch_norm<true, true>(a, s) : launch_norm<true, false>(a, s);
+  else tail ? launch_norm<false, true>(a, s) : launch_norm<false, false>(a, s);
   return hipGetLastError();
 }
 

@@ -11,16 +11,17 @@ struct Raw8 {
   u32x4 a, b;
 };
 
-// The first `valid` of eight values from element `at` on (at any address of the type), zeros behind them.
-template <int DT>
+// The first `valid` of eight values from element `at` on (at any address of the type), zeros behind them. TAIL: a row may end inside
+// eight; else `valid` is 8 or more, or none, and the code for its end is not there (which costs 40 instructions a piece).
+template <int DT, bool TAIL>
 __device__ __forceinline__ void load8(Raw8& r, const void* p, int64_t at, int valid) {
   r.a = r.b = u32x4{0, 0, 0, 0};
   if constexpr (DT == kF32) {
     const float* f = reinterpret_cast<const float*>(p) + at;
-    if (valid >= 8) {
+    if (TAIL ? valid >= 8 : valid > 0) {
       r.a = *reinterpret_cast<const u32x4_any*>(f);
       r.b = *reinterpret_cast<const u32x4_any*>(f + 4);
-    } else {
+    } else if constexpr (TAIL) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < valid) r.a[i] = __builtin_bit_cast(uint32_t, f[i]);
@@ -29,13 +30,25 @@ __device__ __forceinline__ void load8(Raw8& r, const void* p, int64_t at, int va
     }
   } else {
     const uint16_t* h = reinterpret_cast<const uint16_t*>(p) + at;
-    if (valid >= 8) {
+    if (TAIL ? valid >= 8 : valid > 0) {
       r.a = *reinterpret_cast<const u32x4_any*>(h);
-    } else {
+    } else if constexpr (TAIL) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (i < valid) r.a[i >> 1] |= (uint32_t)h[i] << (16 * (i & 1));
     }
+  }
+}
+
+// The first `valid` (more than none) of eight bytes.
+template <bool TAIL>
+__device__ __forceinline__ void store_bytes(uint8_t* q, const uint32_t (&w)[2], int valid) {
+  if (!TAIL || valid >= 8) {
+    *reinterpret_cast<u32x2_any*>(q) = u32x2_any{w[0], w[1]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < valid) q[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
   }
 }
 
@@ -97,27 +110,61 @@ __device__ __forceinline__ uint32_t e4m3_at_border(uint32_t low, uint32_t sign, 
   return sign | (a > b || (a == b && (low & 1)) ? low + 1 : low);
 }
 
-// Four e4m3 steps, the nearest to 448 p / amax, ties to the even code; inv = 448 / amax. The quotient in binary32 is off by
-// less than 2^-22 of itself, so where its neighbours at that distance round to one step, that is the step; else the
-// step is decided exactly (about one value in 10^5 of random ones).
-__device__ __forceinline__ uint32_t e4m3_steps(const double (&p)[4], double inv, double amax) {
-  constexpr float kDown = 1.f - 0x1p-22f, kUp = 1.f + 0x1p-22f;
-  float t[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) t[i] = (float)(p[i] * inv);
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[0] * kDown, t[1] * kDown, 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(t[2] * kDown, t[3] * kDown, lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[0] * kUp, t[1] * kUp, 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(t[2] * kUp, t[3] * kUp, hi, true);
+// Four e4m3 steps from quotients below and above the true ones: where both round to one step, that is the step; else it is
+// decided exactly (about one value in 30000 of random ones). at(i): the value and its amax.
+template <class At>
+__device__ __forceinline__ uint32_t e4m3_between(const float (&below)[4], const float (&above)[4], At at) {
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(below[0], below[1], 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(below[2], below[3], lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(above[0], above[1], 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(above[2], above[3], hi, true);
   uint32_t q = (uint32_t)hi;
   if (lo != hi) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t l = (uint32_t)lo >> (8 * i) & 255u, h = (uint32_t)hi >> (8 * i) & 255u;
-      if (l != h) q = (q & ~(255u << (8 * i))) | e4m3_at_border(l & 127u, h & 128u, p[i], amax) << (8 * i);
+      if (l != h) q = (q & ~(255u << (8 * i))) | at(i, l & 127u, h & 128u) << (8 * i);
     }
   }
   return q;
+}
+
+// The factors that bring a block's values to e4m3 quotients a little below and above the true ones, from its largest magnitude as a
+// binary32 (rounded once). v_rcp_f32 is off by 2^-23 of itself at most; the value, the magnitude, 448 times the reciprocal, the
+// factor and the quotient are rounded by 2^-24 each: 7 * 2^-24 together, less than half of kNear.
+constexpr float kNear = 0x1p-20f;
+struct BlockFactors {
+  float below, above;
+  bool plain;                                    // amax is far from the ends of binary32; else the quotients are formed in binary64
+};
+__device__ __forceinline__ BlockFactors block_factors(float amax) {
+  BlockFactors f;
+  f.plain = amax >= 0x1p-100f && amax <= 0x1p100f;
+  const float inv = kE4m3Max * __builtin_amdgcn_rcpf(amax);
+  f.below = inv * (1.f - kNear);
+  f.above = inv * (1.f + kNear);
+  return f;
+}
+
+// Four steps of values p (or of p rounded once, v) in a block of largest magnitude amax.
+__device__ __forceinline__ uint32_t e4m3_steps(const float (&v)[4], const double (&p)[4], const BlockFactors& f, double amax) {
+  float below[4], above[4];
+  if (f.plain) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      below[i] = v[i] * f.below;
+      above[i] = v[i] * f.above;
+    }
+  } else {
+    const double inv = amax > 0.0 ? (double)kE4m3Max / amax : 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float t = (float)(p[i] * inv);
+      below[i] = t * (1.f - kNear);
+      above[i] = t * (1.f + kNear);
+    }
+  }
+  return e4m3_between(below, above, [&](int i, uint32_t low, uint32_t sign) { return e4m3_at_border(low, sign, p[i], amax); });
 }
 
 }  // namespace tg

@@ -73,7 +73,8 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
   constexpr int U = Slots::U, SLDS = S::XLDS + ST * S::XBUF;
   constexpr bool WIDE = DT == kF32;
   constexpr bool LARGE = AT * RX >= 16;          // registers for one set of operands beside the sums
-  __shared__ __attribute__((aligned(1024))) int8_t sh[SLDS + ST * Slots::BUF];
+  constexpr int LIST = SLDS + ST * Slots::BUF;   // the tile's entries of order
+  __shared__ __attribute__((aligned(1024))) int8_t sh[LIST + (TX < 64 ? 64 : TX) * 4];
   const int lane = threadIdx.x & 63, wave = wave_id();
   const int j = lane & 15, g = lane >> 4;
   const Tile tile = find_tile(a, out_tiles, row_tiles, TX);
@@ -96,13 +97,47 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
   auto wrow = [&](int i) { return S::RPI * (S::LW * wave + i) + lrow; };   // LDS row of this lane in instruction i
   auto xrow = [&](int i) { return S::RPI * (NW * i + wave) + lrow; };
   auto piece = [&](int row) { return 16 * ((lane % (BK / 16)) ^ S::swizzle(row)); };
-  auto source = [&](int i) { return (int64_t)(max(pair_of(a, tile, i), 0) / a.pairs_per_row); };   // activation row of the tile's row i
   // The layer's rows are addressed by 32-bit offsets to the tile's first row (the launch keeps their stride below 2^23).
   const int8_t* wbase = a.w + ((int64_t)tile.expert * a.m + o0) * a.ldw;
   uint32_t woff[S::LW];
-  const int8_t* xp[S::LX];
 #pragma unroll
   for (int i = 0; i < S::LW; ++i) woff[i] = (uint32_t)min(lds_row_output(AT, wrow(i)), a.m - 1 - o0) * (uint32_t)a.ldw;
+  const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)sh;
+  const uint32_t wfill = __builtin_amdgcn_readfirstlane(sh0 + wave * S::LW * 1024);
+  const uint32_t xfill = __builtin_amdgcn_readfirstlane(sh0 + S::XLDS + wave * 1024);
+  const uint32_t sfill = __builtin_amdgcn_readfirstlane(sh0 + SLDS + wave * 256);
+  auto load_w = [&](int step, uint32_t buf, int from, int to) {
+    const int k = step * BK, most = a.n - 16 - k;    // pieces past the end: any bytes of the row, not multiplied
+#pragma unroll
+    for (int i = from; i < to; ++i)
+      load_to_lds(wbase, woff[i] + (uint32_t)(k + min(piece(wrow(i)), most)), wfill + buf * S::WBUF + i * 1024);
+  };
+  const int steps_all = (a.n + BK - 1) / BK;
+  const int begin = (int)((int64_t)steps_all * sp / a.splits), end = (int)((int64_t)steps_all * (sp + 1) / a.splits);
+  int s = begin;
+
+  // The layer's first rows are asked for while the experts' list of the tile's rows is on its way, which the rest of the loads wait
+  // for, and which is kept for the stores.
+  const int* list = reinterpret_cast<const int*>(sh + LIST);
+  if (a.offsets) {
+    constexpr int WAVES = (TX + 63) / 64;        // whose lanes hold the list; the others ask for the same again
+    const int part = wave % WAVES;
+    load4_to_lds(reinterpret_cast<const float*>(a.order + tile.first + min(64 * part + lane, tile.count - 1)), sh0 + LIST + 256 * part);
+  }
+  load_w(begin, 0, 0, S::LW);
+  if (a.offsets) {
+    wait_loads<S::LW>();
+    __builtin_amdgcn_s_barrier();
+  }
+  // Output row (pair) of the tile's row i, or -1, and its activation row.
+  auto pair_at = [&](int i) {
+    if (i >= tile.count) return -1;
+    if (!a.offsets) return tile.first + i;
+    const int p = list[i];
+    return p >= 0 && p < a.M ? p : -1;
+  };
+  auto source = [&](int i) { return (int64_t)(max(pair_at(i), 0) / a.pairs_per_row); };
+  const int8_t* xp[S::LX];
 #pragma unroll
   for (int i = 0; i < S::LX; ++i) xp[i] = a.x + source(xrow(i)) * a.ldx;
   const int blocks = (a.n + 127) >> 7;           // of the inner axis
@@ -116,16 +151,6 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
     sp0 = own ? a.ws + ((int64_t)tile.expert * ((a.m + 127) >> 7) + ob) * blocks
               : a.xs + source(16 * (S::WX * r + uw % S::WX) + vj) * a.ldxs;
   }
-  const uint32_t sh0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int8_t*)sh;
-  const uint32_t wfill = __builtin_amdgcn_readfirstlane(sh0 + wave * S::LW * 1024);
-  const uint32_t xfill = __builtin_amdgcn_readfirstlane(sh0 + S::XLDS + wave * 1024);
-  const uint32_t sfill = __builtin_amdgcn_readfirstlane(sh0 + SLDS + wave * 256);
-  auto load_w = [&](int step, uint32_t buf, int from, int to) {
-    const int k = step * BK, most = a.n - 16 - k;    // pieces past the end: any bytes of the row, not multiplied
-#pragma unroll
-    for (int i = from; i < to; ++i)
-      load_to_lds(wbase, woff[i] + (uint32_t)(k + min(piece(wrow(i)), most)), wfill + buf * S::WBUF + i * 1024);
-  };
   auto load_x = [&](int step, uint32_t buf, int from, int to) {
     const int k = step * BK, most = a.n - 16 - k;
 #pragma unroll
@@ -140,9 +165,6 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
     for (int r = 0; r < RX; ++r) acc[t][r] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int slot = 16 * (g ^ S::swizzle(j));     // of the step's first 64 bytes; the h-th 64: slot ^ 64 h
   const int abase = (wo * 16 * AT + j) * BK + slot, bbase = S::XLDS + (wx * 16 + j) * BK + slot;
-  const int steps_all = (a.n + BK - 1) / BK;
-  const int begin = (int)((int64_t)steps_all * sp / a.splits), end = (int)((int64_t)steps_all * (sp + 1) / a.splits);
-  int s = begin;
   uint32_t buf = 0;                              // of step s
   // Reads of block u of step s.
   auto both = [&](int at, int u) {
@@ -178,13 +200,13 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
     for (int c = 0; c < 4; ++c) sum[c] = fmaf(p[c], scale, sum[c]);
   };
 
-  // A step's loads: W, X, scales. kAhead may still be in flight when the first step's are needed.
+  // A step's loads: W, X, scales; the first W is under way. kAhead may still be in flight when the first step's are needed.
   constexpr int kStep = S::LW + S::LX + 1, kAhead = (ST - 1) * kStep;
   auto first_loads = [&]() {
 #pragma unroll
     for (int i = 0; i < ST; ++i) {
       const int step = min(begin + i, end - 1);
-      load_w(step, i, 0, S::LW);
+      if (i > 0) load_w(step, i, 0, S::LW);
       load_x(step, i, 0, S::LX);
       load_s(step, i);
     }
@@ -499,7 +521,7 @@ __global__ __launch_bounds__(64 * S::NW, S::OCC) void fp8_tile_kernel(const Prod
   const int ob = o0 + 16 * AT * wo;
   int pair[RX];
 #pragma unroll
-  for (int r = 0; r < RX; ++r) pair[r] = pair_of(a, tile, 16 * (S::WX * r + wx) + j);
+  for (int r = 0; r < RX; ++r) pair[r] = pair_at(16 * (S::WX * r + wx) + j);
   constexpr int N = AT == 1 ? 4 : 8;
 #pragma unroll
   for (int r = 0; r < RX; ++r) {

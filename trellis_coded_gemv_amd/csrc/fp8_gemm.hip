@@ -574,7 +574,7 @@ constexpr TileSize kTiles[] = {
 constexpr int kShapes = sizeof(kTiles) / sizeof(kTiles[0]);
 
 // What they cost with 16-bit and with 32-bit outputs, fitted to 14 layers (130 to 28672 outputs, 768 to 20000 inputs) at 1 to 4096
-// rows and 11 sets of experts: microseconds per 128 of the inner axis for a compute unit that holds one workgroup, and for one that
+// rows and 15 sets of experts: microseconds per 128 of the inner axis for a compute unit that holds one workgroup, and for one that
 // holds two; microseconds per tile beside that (its first loads, its stores). Of the product: bytes per microsecond where it
 // waits for memory alone, and the part of the shorter of the two times that the longer does not hide; of a split inner axis:
 // microseconds at all, for each part, and for each value of a part's sums.
@@ -586,15 +586,15 @@ struct Costs {
   float stream, unhidden, join, part, value;
 };
 constexpr Costs kCosts[2] = {
-    {{{1.587f, 1.587f, 5.65f}, {0.988f, 0.988f, 3.33f}, {0.618f, 1.062f, 3.35f}, {0.459f, 0.748f, 2.65f},
-      {0.298f, 0.476f, 2.12f}, {0.168f, 0.326f, 1.91f}, {0.147f, 0.256f, 1.31f}, {0.084f, 0.132f, 2.57f}},
-     7.78e6f, 0.676f, 0.43f, 0.445f, 2.78e-6f},
-    {{{0.f, 0.f, 0.f}, {1.527f, 1.527f, 8.48f}, {0.972f, 1.723f, 5.37f}, {0.590f, 1.084f, 3.57f},
-      {0.384f, 0.668f, 2.49f}, {0.243f, 0.431f, 1.98f}, {0.192f, 0.322f, 1.42f}, {0.135f, 0.194f, 2.31f}},
-     6.39e6f, 0.348f, 0.08f, 0.384f, 2.14e-6f}};
+    {{{1.580f, 1.580f, 4.85f}, {0.959f, 0.959f, 3.62f}, {0.642f, 1.057f, 2.94f}, {0.467f, 0.758f, 2.39f},
+      {0.313f, 0.483f, 2.05f}, {0.177f, 0.331f, 1.72f}, {0.151f, 0.263f, 1.14f}, {0.090f, 0.144f, 2.22f}},
+     7.36e6f, 0.578f, 0.37f, 0.459f, 2.83e-6f},
+    {{{0.f, 0.f, 0.f}, {1.555f, 1.555f, 7.85f}, {0.958f, 1.700f, 5.45f}, {0.601f, 1.079f, 3.59f},
+      {0.394f, 0.668f, 2.59f}, {0.252f, 0.437f, 1.84f}, {0.198f, 0.325f, 1.45f}, {0.142f, 0.192f, 2.23f}},
+     6.33e6f, 0.311f, 0.17f, 0.395f, 2.12e-6f}};
 
 // The cheapest shape and split of the inner axis: rounds of workgroups over the compute units, and the time that the bytes
-// take. Over the sweep this loses 1.5% against trying everything (37% at worst, 9 of 34 us). Experts: row tiles as an even routing
+// take. Over the sweep this loses 1.6% against trying everything (38% at worst, 9 of 34 us). Experts: row tiles as an even routing
 // fills them, one half-filled for each expert; their inner axis stays whole, as their launch has no workspace.
 Int8Plan fp8_plan(int M, int m, int n, int experts, bool wide) {
   const Costs& c = kCosts[wide ? 1 : 0];

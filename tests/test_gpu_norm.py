@@ -72,7 +72,8 @@ OUTS = ["float32", "float16", "bfloat16", "int8", "float8_e4m3fn"]
 
 @pytest.mark.parametrize("rows,n,pad", [(1, 1, 0), (3, 7, 1), (1, 16, 0), (5, 127, 0), (4, 128, 8), (2, 129, 3), (3, 512, 0), (2, 513, 2), (7, 1024, 0),
                                         (2, 1025, 1), (1, 2048, 0), (3, 2056, 0), (2, 4097, 5), (1, 8192, 0), (2, 8200, 0), (3, 16384, 0), (2, 16385, 1),
-                                        (1, 32768, 0), (2, 32767, 3), (600, 4096, 0), (513, 5001, 1), (515, 8192, 0), (66000, 40, 0)])
+                                        (1, 32768, 0), (2, 32767, 3), (600, 4096, 0), (513, 5001, 1), (515, 8192, 0), (520, 10240, 0),
+                                        (514, 10247, 3), (512, 12288, 0), (513, 16383, 1), (3, 24576, 0), (2, 20001, 0), (66000, 40, 0)])
 @pytest.mark.parametrize("out", OUTS)
 @pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
 def test_rows(rows, n, pad, out, dtype):

@@ -18,8 +18,10 @@ namespace {
 
 // The int8 step nearest to 127 p / amax, halves to the even one; inv = 127 / amax. t is off by at most 2^-44: unless it lies
 // that near to a half, its nearest whole number is the step. Else 254 |p| is compared with (2 k + 1) amax, of products in two
-// parts, as they have up to 56 bits.
+// parts, as they have up to 56 bits: a and b are rounded, and what they lack is added behind their difference. So a - b has to take a as it
+// was rounded: fused into fma(254, |p|, -b) it would hold what a lacks already, and decide ties by it.
 __device__ __forceinline__ int int8_step(double p, double inv, double amax) {
+#pragma clang fp contract(off)
   const double t = p * inv, k = rint(t);
   if (fabs(fabs(t - k) - 0.5) > 0x1p-30) return (int)k;
   const double low = floor(fabs(t)), odd = 2.0 * low + 1.0;

@@ -317,3 +317,25 @@ def test_workspace_refusals_on_the_device():
         tg.fp8_gemm(L, q, s.t().contiguous().t())                   # a row's scales apart
     with pytest.raises(tg.TgError):
         tg.fp8_gemm(L, q[:1].expand(61, 8192), s)                   # rows that share their memory
+
+
+def test_experts_from_dense_on_a_stream():
+    """Made on a named stream while the current one still writes memory that it has given back."""
+    dev = device()
+    import torch
+    say("fp8 experts from dense on a stream")
+    weight = torch.randn(4, 1024, 2048, generator=torch.Generator().manual_seed(6)).to(dev)
+    want = tg.Fp8Experts.from_dense(weight)
+    a, big = torch.cuda.Stream(), torch.randn(4096, 4096, device=dev)
+    torch.cuda.synchronize()
+    for stream in (a, a.cuda_stream, a):
+        given_back = [torch.empty(4, 1024, 2048, dtype=torch.uint8, device=dev), torch.empty(4, 8, 16, device=dev)]
+        for _ in range(4):
+            big @ big                                               # the writes below come after this
+        for t in given_back:
+            t.fill_(77)
+        del given_back, t
+        E = tg.Fp8Experts.from_dense(weight, stream=stream)
+        a.synchronize()
+        q, s = E.q.view(torch.uint8).clone(), E.scales.clone()
+        assert torch.equal(q, want.q.view(torch.uint8)) and torch.equal(s, want.scales)

@@ -932,11 +932,15 @@ class Fp8Experts:
         """The nearest e4m3 experts of dense weights [experts, m, n]."""
         torch = _torch()
         _expect(weight.dim() == 3, "Fp8Experts", "expected weights [experts, m, n]")
+        at = _common_device("Fp8Experts", weight)
+        if stream is not None or at != torch._C._cuda_getDevice():
+            with _Entered(at, stream):                              # before the allocations, which are the entered stream's
+                return cls.from_dense(weight)
         experts, m, n = weight.shape
         q = torch.empty(experts, m, n, dtype=torch.float8_e4m3fn, device=weight.device)
         scales = torch.empty(experts, _blocks(m), _blocks(n), dtype=torch.float32, device=weight.device)
         for e in range(experts):
-            fp8_quantize(weight[e], q[e], scales[e], _FP8_BLOCK, stream)
+            fp8_quantize(weight[e], q[e], scales[e], _FP8_BLOCK)
         return cls(q, scales)
 
 

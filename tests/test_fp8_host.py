@@ -1,5 +1,6 @@
 """What the norm and e4m3 calls of the binding do on the host, watched without a device."""
 import contextlib
+import threading
 
 import pytest
 
@@ -49,3 +50,28 @@ def test_experts_are_allocated_on_the_stream_that_fills_them(stream, monkeypatch
     where = [] if stream is None else [(0, stream)]
     assert allocated == [where] * 2 and filled == [where] * 3
     assert experts.q.shape == (3, 130, 144) and experts.scales.shape == (3, 2, 2)
+
+
+def test_a_second_thread_finds_the_output_types_whole(monkeypatch):
+    """rms_norm's table of output types is made by its first call: a call of another thread meanwhile finds none of it or all."""
+    torch = pytest.importorskip("torch")
+    failures = []
+
+    def call(out_dtype):
+        try:
+            tg.rms_norm(torch.zeros(2, 8), torch.zeros(8), out_dtype=out_dtype)
+        except ValueError as e:                                     # on a host tensor: the device is refused, behind the type
+            if "on a GPU" not in str(e):
+                failures.append(str(e))
+
+    class Watched(dict):
+        def update(self, *a):
+            super().update(*a)
+            if threading.current_thread() is threading.main_thread():
+                for out_dtype in (torch.float32, torch.float16, torch.bfloat16, torch.int8, torch.float8_e4m3fn):
+                    t = threading.Thread(target=call, args=(out_dtype,))
+                    t.start()
+                    t.join()
+    monkeypatch.setattr(tg, "_OUT_TYPES", Watched())
+    call(torch.float32)
+    assert not failures and len(tg._OUT_TYPES) == 5

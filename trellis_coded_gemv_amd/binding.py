@@ -772,9 +772,8 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype=None, total=
     torch = _torch()
     w = "rms_norm"
     dtype = _dtype_code(x.dtype, w)
-    if not _OUT_TYPES:
-        _OUT_TYPES.update(_DTYPES)
-        _OUT_TYPES.update({torch.int8: 3, torch.float8_e4m3fn: 4})
+    if not _OUT_TYPES:                                              # in one update: another thread finds all of it or none
+        _OUT_TYPES.update({**_DTYPES, torch.int8: 3, torch.float8_e4m3fn: 4})
     if out_dtype is None:
         out_dtype = x.dtype if y is None else y.dtype
     out = _OUT_TYPES.get(out_dtype)

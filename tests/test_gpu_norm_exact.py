@@ -1,4 +1,5 @@
-"""rms_norm where its decisions are closest: int8 ties of products with 48 significant bits."""
+"""rms_norm where its decisions are closest: int8 ties of products with 48 significant bits, values that only a
+large weight brings back into the range."""
 import numpy as np
 import pytest
 
@@ -48,3 +49,43 @@ def test_int8_products_one_unit_from_a_tie():
             a = odd * int(c)
             _int8(torch, np.array([[254.0 * c, a - 1, -(a - 1), a, -a]]), np.array([a, a + 1, a + 1, a, a]) * 2.0 ** -20)
             _int8(torch, np.array([[254.0 * c, a + 1, -(a + 1), a, -a]]), np.array([a + 2, a + 1, a + 1, a + 2, a + 2]) * 2.0 ** -20)
+
+
+@pytest.mark.parametrize("out", ["float32", "bfloat16"])
+@pytest.mark.parametrize("n", [2, 13, 304, 4100])
+def test_weights_that_bring_small_values_back(n, out):
+    """Values that the norm alone takes below binary32's normal range, with weights up to 2^127: every output keeps its bits, on rows of
+    every scale."""
+    dev = device()
+    import torch
+    say("norm small values, large weights", n, out)
+    rng = np.random.default_rng(n)
+    rows = []
+    for row in (0, 60, 100, -60, -110):                             # the row's largest values
+        h = np.ldexp(1 + rng.random(n), row - rng.integers(90, 149, n))
+        h[0] = np.ldexp(1.0, row)
+        rows.append(h * rng.choice([-1, 1], n))
+    x = torch.from_numpy(np.array(rows).astype(np.float32))
+    w = np.ldexp(1 + rng.random(n), rng.integers(60, 127, n))
+    w[0], w[1] = 1.0, 1.3 * 2.0 ** 127
+    x[0, 1] = 2.0 ** -130
+    w = torch.from_numpy(w.astype(np.float32))
+    y = tg.rms_norm(x.to(dev), w.to(dev), eps=0.0, out_dtype=getattr(torch, out))
+    torch.cuda.synchronize()
+    for r in range(len(x)):
+        _check(torch, x[r:r + 1].to(dev), w.to(dev), None, 0.0, out, y[r:r + 1], None, None)
+
+
+@pytest.mark.parametrize("out", ["float32", "float16"])
+def test_zeros_beside_values_whose_norm_leaves_binary32(out):
+    """Pieces of zeros in a row of subnormal values, whose 1 / sqrt(mean) is beyond binary32: zeros stay zeros."""
+    dev = device()
+    import torch
+    say("norm zeros beside subnormal values", out)
+    x = torch.zeros(2, 400)
+    x[0, 5], x[1, 300:] = 2.0 ** -149, -(2.0 ** -140)
+    w = torch.linspace(0.5, 1.5, 400)
+    y = tg.rms_norm(x.to(dev), w.to(dev), eps=0.0, out_dtype=getattr(torch, out))
+    torch.cuda.synchronize()
+    for r in range(2):
+        _check(torch, x[r:r + 1].to(dev), w.to(dev), None, 0.0, out, y[r:r + 1], None, None)

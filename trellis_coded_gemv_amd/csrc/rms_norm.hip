@@ -228,7 +228,10 @@ __global__ __launch_bounds__(THREADS) void rms_norm_kernel(const NormArgs a) {
   const float inv32 = (float)inv;
   const double step = r / (double)kE4m3Max;
   const float r32 = (float)r;
-  const bool in_range = r >= 0x1p-120 && r <= 0x1p120;   // so h r32 is a normal number, or nothing beside the row's others
+  // Where every h r32 is zero or a normal number, y is formed in binary32; else in binary64, as a large weight may bring back what a
+  // subnormal one loses. `least`: bits of the smallest such |h|, less one.
+  const bool in_range = r >= 0x1p-120 && r <= 0x1p120;
+  const uint32_t least = max(__builtin_bit_cast(uint32_t, (float)(0x1p-125 / r)), 1u) - 1u;
 
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -292,8 +295,16 @@ __global__ __launch_bounds__(THREADS) void rms_norm_kernel(const NormArgs a) {
     } else {
       if (valid <= 0) break;
       float y[8];
+      uint32_t low = 0xFFFFFFFFu;                // zeros count as large
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = in_range ? h[e] * r32 * w[e] : (float)((double)h[e] * (double)w[e] * r);
+      for (int e = 0; e < 8; ++e) low = min(low, (__builtin_bit_cast(uint32_t, h[e]) & 0x7FFFFFFFu) - 1u);
+      if (in_range && low >= least) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = h[e] * r32 * w[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = (float)((double)h[e] * (double)w[e] * r);
+      }
       Raw8 bits;
       narrow<false>(y, a.out, bits);
       store8<false, TAIL>(bits, a.out, a.y, to, valid);

@@ -1,9 +1,10 @@
 """rms_norm where its decisions are closest: int8 ties of products with 48 significant bits, values that only a
-large weight brings back into the range."""
+large weight brings back into the range, the borders of the steps and the values beside them."""
 import numpy as np
 import pytest
 
 from gpu_common import device, say
+from oracle import fp8
 from test_gpu_norm import _check
 from trellis_coded_gemv_amd import binding as tg
 
@@ -89,3 +90,35 @@ def test_zeros_beside_values_whose_norm_leaves_binary32(out):
     torch.cuda.synchronize()
     for r in range(2):
         _check(torch, x[r:r + 1].to(dev), w.to(dev), None, 0.0, out, y[r:r + 1], None, None)
+
+
+def _neighbours(torch, v):
+    """v, and the values of its type one last place above and below in magnitude."""
+    bits = v.view(torch.int32 if v.dtype == torch.float32 else torch.int16)
+    return [v, (bits + 1).view(v.dtype), (bits - 1).view(v.dtype)]
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("out", ["int8", "float8_e4m3fn"])
+def test_every_border_and_its_neighbours(out, dtype):
+    """Every border of two steps and the values of the type one last place beside it, at scales that are powers of two or not; every row compared."""
+    dev = device()
+    import torch
+    say("norm borders and neighbours", out, dtype)
+    t = getattr(torch, dtype)
+    m = fp8.magnitudes()
+    top, mid = (127.0, np.arange(0.5, 127)) if out == "int8" else (448.0, (m[1:] + m[:-1]) / 2)
+    rows = []
+    for scale in (1.0, 2.0 ** -5, 3.0, 2.0 ** 5 / 3):
+        border = torch.from_numpy(mid * scale).to(t)
+        for v in _neighbours(torch, border):
+            rows += [torch.cat([torch.full((1,), top * scale, dtype=t), v]), torch.cat([torch.full((1,), -top * scale, dtype=t), -v])]
+    x = torch.stack(rows)
+    parts = [torch.cat([x[:, :1], p, x[:, :1].expand(-1, 127 - p.shape[1])], 1) for p in x[:, 1:].split(127, 1)]   # each 128 values with the largest among them
+    x = torch.cat(parts, 1).contiguous().to(dev)
+    for w in (1.0, 1.0 + 2.0 ** -7, 1.0 + 3 * 2.0 ** -5):
+        w = torch.full((x.shape[1],), w, dtype=t, device=dev)
+        got = tg.rms_norm(x, w, out_dtype=getattr(torch, out))
+        torch.cuda.synchronize()
+        for r in range(x.shape[0]):
+            _check(torch, x[r:r + 1], w, None, EPS, out, got[0][r:r + 1], got[1][r:r + 1], None)

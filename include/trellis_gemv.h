@@ -621,8 +621,9 @@ int32_t fp8_quantize(int32_t rows, int32_t n, const void *x, int32_t dtype, int6
  * the same call gives the same bits. A TG_F32 output has sums of binary32 throughout. The sums behind a 16-bit output are the
  * matrix cores' 8-bit ones, which align eight neighbouring products to the largest exponent among them and drop what lies below
  * 2^-13 of it: off by 2^-10 of the sum of the products' magnitudes at most (2^-7 where a largest product has a subnormal factor), and
- * by about 2^-16 of the result on values that fp8_quantize scaled. A NaN or an infinity in a row, a layer or their scales reaches the
- * outputs that it takes part in.
+ * by about 2^-16 of the result on values that fp8_quantize scaled. The product of a block's two scales is formed first, in binary32: it
+ * has to be zero or lie in 2^-126 .. 2^128, as a smaller one loses bits and a larger one is an infinity (NaN with a sum of zero). A
+ * NaN or an infinity in a row, a layer or their scales reaches the outputs that it takes part in.
  *   M, m, n : as for int8_gemm.
  *   xq : device, M rows of n e4m3 values, 16-byte aligned, row stride ldx >= n bytes, a multiple of 16.
  *   xs : device, M rows of ceil(n / 128) fp32, row stride ldxs.

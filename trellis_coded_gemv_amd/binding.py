@@ -972,7 +972,8 @@ def _fp8_rows(torch, where: str, n: int, xq, xs):
 
 def fp8_gemm(layer: "Fp8Layer", xq, xs, Y=None, out_dtype=None, ws=None, stream=None):
     """Y [M, m] = sum over blocks b of 128 inputs of (xq_b wq_b^T) * xs[r, b] * scales[o // 128, b], of e4m3 rows xq [M, n] with scales
-    xs [M, ceil(n / 128)]; out_dtype (or Y's type) float32, float16 or bfloat16."""
+    xs [M, ceil(n / 128)]; out_dtype (or Y's type) float32, float16 or bfloat16. The products of two scales, each formed in binary32, have
+    to be zero or normal numbers."""
     torch = _torch()
     w = "fp8_gemm"
     m, n = layer.m, layer.n
@@ -997,7 +998,7 @@ def fp8_gemm(layer: "Fp8Layer", xq, xs, Y=None, out_dtype=None, ws=None, stream=
 
 def fp8_gemm_grouped(experts: "Fp8Experts", xq, xs, offsets, order, pairs_per_row: int = 1, Y=None, out_dtype=None, stream=None):
     """Y [pairs, m]: row p = order[j], offsets[e] <= j < offsets[e + 1], is expert e's product with the e4m3 row
-    xq[p // pairs_per_row] and its scales. Rows of pairs without an expert, which order lists behind offsets[-1], are zero in an output
+    xq[p // pairs_per_row] and its scales, which are as fp8_gemm's. Rows of pairs without an expert, which order lists behind offsets[-1], are zero in an output
     that the call makes, and left as they were in a Y of the caller's."""
     torch = _torch()
     w = "fp8_gemm_grouped"

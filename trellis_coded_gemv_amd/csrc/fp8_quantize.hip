@@ -1,7 +1,7 @@
 // e4m3 rows with a scale for each 128 values, and e4m3 layers with a scale for each block of 128 x 128:
 //     amax = max |x_i| of the block, scale = amax / 448, q_i = the e4m3 value nearest to 448 x_i / amax.
 // Bound by memory: 8192 x 8192 fp16 (203 MB) 38.6 us, 5.2 TB/s, where a large copy moves 4.9 to 5.1; 4096 x 14336 bf16 (178 MB) 37.7
-// us, binary32 53 us (5.5 TB/s); a layer of 28672 x 8192 bf16 (705 MB) 127 us. One row of 8192 takes 2.3 us. Quotients and scales
+// us, binary32 53 us (5.5 TB/s; the same rows again and again 32, 35 and 44 us); a layer of 28672 x 8192 bf16 (705 MB) 127 to 139 us. One row of 8192 takes 2.3 us. Quotients and scales
 // by binary64 divisions and one block to a lane took 41.2 us for 4096 x 14336, four blocks to a lane 39.3.
 #include "product_tiles.hpp"
 #include "rows8.hpp"

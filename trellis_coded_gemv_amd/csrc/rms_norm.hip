@@ -4,8 +4,8 @@
 // with T = 127 and amax the row's largest |p| (int8), or T = 448 and that of each 128 values (e4m3). The norm scales a row as a
 // whole, so the steps do not depend on it: they are decided on the exact products p, which binary64 holds.
 //
-// Bound by memory: 8192 x 8192 bf16 with a residual into e4m3 (472 MB) 93.3 us, 5.05 TB/s, where a large copy moves 4.9 to 5.1; into
-// bf16 (537 MB) 103.7 us; into int8 with binary32 weights 112 us, where the instructions show. A row of which no thread sees an
+// Bound by memory: 8192 x 8192 bf16 with a residual into e4m3 (472 MB) 93 to 98 us, 5.0 TB/s, where a large copy moves 4.9 to 5.1; into
+// bf16 (537 MB) 102 to 105 us; into int8 with binary32 weights 113 us, where the instructions show. A row of which no thread sees an
 // end inside eight values has code without it: with that code 125, 124 and 121 us. One row of 8192 takes 4.1 us.
 #include <type_traits>
 
@@ -318,8 +318,8 @@ static void launch_norm(const NormArgs& a, hipStream_t s) {
   const unsigned x = a.rows < 65536 ? (unsigned)a.rows : 65536u;
   const dim3 grid(x, ((unsigned)a.rows + x - 1) / x);
   // A row is a wave's up to 1024 values. Longer ones: of many rows, the fewest threads that hold it (4096 x 10240 bf16 with a residual,
-  // into e4m3: 256 threads 69.7 us, 512 72.3, 1024 93.8; 2000 x 15000: 115, 78 and 98); of few, as many as there are pieces
-  // (1 x 16384: 11.1, 7.5 and 6.5).
+  // into e4m3: 256 threads 69.7 us, 512 72.3, 1024 93.8; 2000 x 15000 fp32 with a bf16 residual, into int8: 115, 78 and 98); of few, as
+  // many as there are pieces (1 x 16384: 11.1, 7.5 and 6.5).
   const bool many = a.rows >= 512;
   if (pieces <= 64) hipLaunchKernelGGL((rms_norm_kernel<64, 1, NARROW, TAIL>), grid, dim3(64), 0, s, a);
   else if (pieces <= 128) hipLaunchKernelGGL((rms_norm_kernel<64, 2, NARROW, TAIL>), grid, dim3(64), 0, s, a);

@@ -186,7 +186,8 @@ __global__ __launch_bounds__(THREADS) void rms_norm_kernel(const NormArgs a) {
   }
   const bool finite = sum < __builtin_inf();     // a square of finite binary32 values is far from the end of binary64
   const double mean = sum / (double)a.n + (double)a.eps;
-  const double r = !finite ? __builtin_nan("") : mean > 0.0 ? 1.0 / sqrt(mean) : 0.0;
+  const double root = sqrt(mean);
+  const double r = !finite ? __builtin_nan("") : mean > 0.0 ? 1.0 / root : 0.0;
 
   // int8: the row's largest product. It is what binary32 says of products of 16-bit values in its range; of wider ones, it is the
   // largest of those that are rounded to what binary32 says; out of its range, the largest of all in binary64 (every thread alike).
@@ -231,7 +232,7 @@ __global__ __launch_bounds__(THREADS) void rms_norm_kernel(const NormArgs a) {
   // Where every h r32 is zero or a normal number, y is formed in binary32; else in binary64, as a large weight may bring back what a
   // subnormal one loses. `least`: bits of the smallest such |h|, less one.
   const bool in_range = r >= 0x1p-120 && r <= 0x1p120;
-  const uint32_t least = max(__builtin_bit_cast(uint32_t, (float)(0x1p-125 / r)), 1u) - 1u;
+  const uint32_t least = max(__builtin_bit_cast(uint32_t, (float)(0x1p-125 * root)), 1u) - 1u;
 
 #pragma unroll
   for (int i = 0; i < PER; ++i) {

@@ -998,8 +998,8 @@ def fp8_gemm(layer: "Fp8Layer", xq, xs, Y=None, out_dtype=None, ws=None, stream=
 
 def fp8_gemm_grouped(experts: "Fp8Experts", xq, xs, offsets, order, pairs_per_row: int = 1, Y=None, out_dtype=None, stream=None):
     """Y [pairs, m]: row p = order[j], offsets[e] <= j < offsets[e + 1], is expert e's product with the e4m3 row
-    xq[p // pairs_per_row] and its scales, which are as fp8_gemm's. Rows of pairs without an expert, which order lists behind offsets[-1], are zero in an output
-    that the call makes, and left as they were in a Y of the caller's."""
+    xq[p // pairs_per_row] and its scales, which are as fp8_gemm's. Rows of pairs without an expert, which order lists behind
+    offsets[-1], are zero in an output that the call makes, and left as they were in a Y of the caller's."""
     torch = _torch()
     w = "fp8_gemm_grouped"
     m, n, count = experts.m, experts.n, experts.experts
